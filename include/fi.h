@@ -76,16 +76,24 @@ typedef enum {
   FI_ERR_CUDA = 4,                /* a CUDA call failed; see fi_last_error_string() */
   FI_ERR_DEVICE_TIMEOUT = 5,      /* a kernel's bounded wait ran out */
   FI_ERR_DEVICE_BOUNDS = 6,       /* a kernel met a page index outside the cache */
-  FI_ERR_NO_DEVICE = 7            /* no usable CUDA device for a run call */
+  FI_ERR_NO_DEVICE = 7,           /* no usable CUDA device for a run call */
+  FI_ERR_OUT_OF_PAGES = 8         /* fi_page_table_step: too few free pages, or a full output */
 } fi_status;
 
 typedef enum { FI_LAYOUT_NHD = 0, FI_LAYOUT_HND = 1 } fi_kv_layout;
 typedef enum { FI_MODE_DECODE = 0, FI_MODE_PREFILL = 1 } fi_mode;
 
 /* Element types: q and out are bf16 or fp16; the K/V cache is the same type
- * or FP8 E4M3 (OCP format; decode plans only). lse and partial states are
+ * or FP8 E4M3 (OCP format): FI_DTYPE_E4M3 with a scale per tensor and kv head
+ * (decode plans only), FI_DTYPE_E4M3_PAGE with a scale for each (page, kv
+ * head) of K and of V (decode and prefill plans). lse and partial states are
  * fp32. */
-typedef enum { FI_DTYPE_BF16 = 0, FI_DTYPE_FP16 = 1, FI_DTYPE_E4M3 = 2 } fi_dtype;
+typedef enum {
+  FI_DTYPE_BF16 = 0,
+  FI_DTYPE_FP16 = 1,
+  FI_DTYPE_E4M3 = 2,
+  FI_DTYPE_E4M3_PAGE = 3
+} fi_dtype;
 
 /*
  * Options of a plan. Start from FI_PLAN_OPTIONS_DEFAULT (a zero-filled
@@ -101,7 +109,11 @@ typedef enum { FI_DTYPE_BF16 = 0, FI_DTYPE_FP16 = 1, FI_DTYPE_E4M3 = 2 } fi_dtyp
  *   kv_dtype     fi_dtype of the K/V cache: -1 = dtype, or FI_DTYPE_E4M3 for
  *                an FP8 cache (decode plans only; FI_ERR_UNSUPPORTED for
  *                prefill plans). An FP8 cache holds K / k_scale and
- *                V / v_scale; the run calls take the two scales.
+ *                V / v_scale; the run calls take the two scales. Or
+ *                FI_DTYPE_E4M3_PAGE for an FP8 cache with page scales (either
+ *                mode): page p of kv head h holds K / s and V / s' with its
+ *                own s = k_head_scale[p * num_kv_heads + h] and s' from
+ *                v_head_scale; fi_append_paged_kv fills such a cache.
  *   num_prefix_groups, prefix_group_indptr, prefix_pages
  *                shared-prefix (cascade) decode: the "FlashInfer kernel
  *                library deep-dive" page, section "batch layer", lists
@@ -186,8 +198,8 @@ typedef struct {
  * than INT32_MAX / 2 keys, more than INT32_MAX query rows in all, shared-
  * prefix groups out of order or whose prefix is not made of full pages of
  * every request in the group),
- * FI_ERR_UNSUPPORTED (head_dim, page_size or g not built; an FP8 cache in a
- * prefill plan; shared prefixes with an FP8 cache, a window or a prefill
+ * FI_ERR_UNSUPPORTED (head_dim, page_size or g not built; an FI_DTYPE_E4M3
+ * cache in a prefill plan; shared prefixes with an FP8 cache, a window or a prefill
  * plan).
  */
 fi_status fi_plan(int32_t mode, int32_t batch_size, const int32_t* qo_indptr_h,
@@ -212,7 +224,9 @@ fi_status fi_plan_get_info(fi_plan_t plan, fi_plan_info* info);
  * slots of that page lie outside the item's window. Decode items come
  * first, then prefill items, then shared-prefix items (request = 2 x the
  * group index, keys within the group's prefix, slot = the state slot of
- * row 0 of q).
+ * row 0 of q). The prefill items of an FI_DTYPE_E4M3_PAGE plan name a kv_head
+ * with all its query heads, too: 256 / g rows of q per item (128 / g at
+ * head_dim 256).
  * `capacity` is in items; *num_items receives the plan's item count.
  */
 fi_status fi_plan_get_work(fi_plan_t plan, int32_t* items_h, int32_t capacity,
@@ -442,10 +456,141 @@ fi_status fi_merge_states(const float* v, const float* s, int32_t n, int32_t S, 
                           int32_t d, int32_t out_dtype, void* out, float* lse_out, void* stream);
 
 /*
+ * The two calls below prepare a serving step on the device: its page table
+ * from the requests' lengths, and the new rows' places in the cache. They
+ * read no host array, copy nothing from the host and may be captured into a
+ * CUDA graph; a replay works on what the device arrays then hold.
+ *
+ * Both take a step workspace: FI_STEP_WORKSPACE_BYTES of device memory,
+ * 256-byte aligned, zero-filled by the caller before its first use (not the
+ * workspace of a run call). Its status word is kept until
+ * fi_check_device_status reads and clears it. Calls that share one must be
+ * ordered (one stream, or events): two that run at once need two.
+ */
+#define FI_STEP_WORKSPACE_BYTES 256
+
+/*
+ * fi_page_table_step — advances requests by one step: takes pages from (or
+ * gives them back to) a ring of free pages and builds the step's page table,
+ * row offsets and slot map ("FlashInfer kernel library deep-dive", section
+ * "PageAttention": pages allocated on demand).
+ *
+ * A request lives in a slot: kv_len[slot] tokens, whose pages are the first
+ * ceil(kv_len / page_size) entries of row `slot` of block_table. Row b of
+ * the step adds new_len[b] tokens to the request in slots[b] (or drops
+ * -new_len[b] of its last ones: rejected draft tokens, or all of them when
+ * it ends); a negative slots[b] is a padding row, an empty request. Let
+ * len = kv_len + new_len, rows = max(new_len, 0). Then, in batch order,
+ *   - the pages that len needs beyond those the request has come from the
+ *     head of the ring: page i of the step is free_ring[(head + i) % cap];
+ *   - the pages it no longer needs go to the tail, in their order in the row:
+ *     free_ring[(head + count + i) % cap];
+ *   - page_indptr [batch+1], page_indices, last_page_len [batch] are the page
+ *     table of all len tokens, qo_indptr [batch+1] the offsets of the rows,
+ *     as the run calls take them (len 0: no pages, last_page_len 0);
+ *   - row i of request b stands at token position kv_len + i: positions
+ *     receives it, slot_map receives page * page_size + slot;
+ *   - kv_len_out[slots[b]] = len, ring_state_out = {new head, new count}.
+ * The entries of slot_map and positions behind the last row, up to
+ * token_capacity, become -1 and 0 (rows of a padded batch). Entries of
+ * block_table and free_ring that are not named above, entries of
+ * page_indices behind the last one and kv_len_out of other slots stay as
+ * they were.
+ *   batch            rows of the step, 0 .. 8192 (0: nothing is done).
+ *   slots            device int32 [batch], or NULL: row b is slot b.
+ *   new_len          device int32 [batch].
+ *   max_requests     slots, 1 .. 262144; max_pages: entries per row of
+ *                    block_table; page_size 1 .. 1024.
+ *   kv_len           device int32 [max_requests]; kv_len_out the same, and
+ *                    may be kv_len itself.
+ *   block_table      device int32 [max_requests][max_pages], in and out.
+ *   free_ring        device int32 [ring_capacity], in and out.
+ *   ring_state       device int32 {head, count}; ring_state_out the same,
+ *                    and may be ring_state itself.
+ *   page_indices     device int32 [page_capacity].
+ *   slot_map         device int64 [token_capacity]; positions: device int32
+ *                    [token_capacity] or NULL.
+ *   workspace        a step workspace (above).
+ * A step that cannot be made changes nothing: its outputs are those of an
+ * empty batch (zero offsets and lengths, slot_map -1), kv_len_out of the
+ * slots and ring_state_out are the old values, and fi_check_device_status
+ * reports FI_ERR_OUT_OF_PAGES (too few free pages, more pages than
+ * page_capacity or max_pages, more rows than token_capacity) or
+ * FI_ERR_DEVICE_BOUNDS (a slot >= max_requests or named twice, a length
+ * below 0 or above INT32_MAX / 2, a ring state outside the ring, more pages
+ * returned than fit it).
+ * Page ids are copied as they are: the calls that use them check them.
+ * Errors: FI_ERR_INVALID_ARG (sizes outside the ranges above, NULL or
+ * misaligned pointers), FI_ERR_WORKSPACE_TOO_SMALL, FI_ERR_NO_DEVICE,
+ * FI_ERR_CUDA.
+ */
+fi_status fi_page_table_step(int32_t batch, const int32_t* slots, const int32_t* new_len,
+                             int32_t max_requests, int32_t max_pages, int32_t page_size,
+                             const int32_t* kv_len, int32_t* kv_len_out, int32_t* block_table,
+                             int32_t* free_ring, int32_t ring_capacity,
+                             const int32_t* ring_state, int32_t* ring_state_out,
+                             int32_t* page_indptr, int32_t* page_indices, int32_t page_capacity,
+                             int32_t* last_page_len, int32_t* qo_indptr, int64_t* slot_map,
+                             int32_t* positions, int32_t token_capacity, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * fi_append_paged_kv — stores new K and V rows in a paged cache.
+ *
+ * Row t goes to page slot_map[t] / page_size, slot slot_map[t] % page_size;
+ * a negative entry is skipped (a padded row). An FI_DTYPE_BF16 / FP16 cache
+ * (kv_dtype = dtype) receives the rows as they are. An FI_DTYPE_E4M3_PAGE
+ * cache receives codes: for every page and kv head with new rows, and for K
+ * and V each,
+ *     s' = the smallest power of two >= 2^-100 with |x| <= 448 s' for the
+ *          finite elements x of the new rows,
+ *     scale = s' if the first new row is slot 0 of the page (what the page
+ *          held before is dropped), else max(scale, s'),
+ *     code = x / scale rounded to E4M3, to nearest even (NaN for NaN and
+ *          infinities);
+ * where the scale grew, the codes of the page's older rows (the slots before
+ * the first new one) become code * old scale / scale, rounded alike. A power
+ * of two makes both divisions exact, so that a page's growth costs its older
+ * rows nothing but what falls below E4M3's smallest values; E4M3 is a
+ * floating-point type, so a scale up to twice as large as needed costs no
+ * relative precision either.
+ * Caller contract for FI_DTYPE_E4M3_PAGE: the new rows of one page are
+ * consecutive rows of the call with consecutive slots (as the slot map of
+ * fi_page_table_step has them). Rows that break it get codes of one of the
+ * scales computed for the page; no two rows may name the same slot.
+ *   num_tokens       rows, >= 0 (0: nothing is done).
+ *   slot_map         device int64 [num_tokens].
+ *   k_new, v_new     device rows of `dtype` (bf16 or fp16), row t at t *
+ *                    token_stride_elems (0 = dense: num_kv_heads * head_dim;
+ *                    a larger one reads k and v out of a fused projection's
+ *                    output), [num_kv_heads][head_dim] each; 16-byte aligned,
+ *                    the stride a multiple of 8.
+ *   k_cache, v_cache, kv_layout, page_stride_elems, num_pages, page_size as
+ *                    for the run calls (head_dim 64, 128, 256; page_size 16,
+ *                    32).
+ *   k_page_scale, v_page_scale  device fp32 [num_pages][num_kv_heads] in and
+ *                    out for FI_DTYPE_E4M3_PAGE (finite and > 0 where a page
+ *                    is part-filled); ignored otherwise.
+ *   workspace        a step workspace (above). A slot outside the cache is
+ *                    skipped and reported as FI_ERR_DEVICE_BOUNDS.
+ * Errors: FI_ERR_INVALID_ARG, FI_ERR_UNSUPPORTED (shapes not built; a
+ * kv_dtype of FI_DTYPE_E4M3), FI_ERR_WORKSPACE_TOO_SMALL, FI_ERR_NO_DEVICE,
+ * FI_ERR_CUDA.
+ */
+fi_status fi_append_paged_kv(int32_t num_tokens, const int64_t* slot_map, const void* k_new,
+                             const void* v_new, int64_t token_stride_elems, int32_t dtype,
+                             int32_t num_kv_heads, int32_t head_dim, void* k_cache,
+                             void* v_cache, int32_t kv_dtype, int32_t kv_layout,
+                             int64_t page_stride_elems, int32_t num_pages, int32_t page_size,
+                             float* k_page_scale, float* v_page_scale, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
  * fi_check_device_status — synchronises `stream`, reads and clears the
  * device error word kept at the start of `workspace` by the runs that used
- * it. Returns FI_OK, FI_ERR_DEVICE_TIMEOUT (a bounded wait ran out) or
- * FI_ERR_DEVICE_BOUNDS (a page index outside the cache was skipped), or
+ * it. Returns FI_OK, FI_ERR_DEVICE_TIMEOUT (a bounded wait ran out),
+ * FI_ERR_DEVICE_BOUNDS (a page index outside the cache was skipped; a
+ * malformed step) or FI_ERR_OUT_OF_PAGES (fi_page_table_step), or
  * FI_ERR_CUDA if the synchronisation itself failed.
  */
 fi_status fi_check_device_status(void* workspace, void* stream);

@@ -24,10 +24,14 @@ FI_ERR_CUDA = 4
 FI_ERR_DEVICE_TIMEOUT = 5
 FI_ERR_DEVICE_BOUNDS = 6
 FI_ERR_NO_DEVICE = 7
+FI_ERR_OUT_OF_PAGES = 8
 
 FI_DTYPE_BF16 = 0
 FI_DTYPE_FP16 = 1
 FI_DTYPE_E4M3 = 2
+FI_DTYPE_E4M3_PAGE = 3
+
+FI_STEP_WORKSPACE_BYTES = 256
 
 FI_LAYOUT_NHD = 0
 FI_LAYOUT_HND = 1
@@ -41,7 +45,8 @@ EXPORTED = ["fi_plan", "fi_plan_destroy", "fi_plan_get_info", "fi_plan_get_work"
             "fi_batch_decode_paged", "fi_batch_prefill_paged", "fi_merge_states",
             "fi_check_device_status", "fi_status_string", "fi_last_error_string",
             "fi_debug_set_fault", "fi_profile_next_launch", "fi_batch_decode_paged_noalloc",
-            "fi_batch_attention_host", "fi_batch_attention_host_async", "fi_host_step_wait"]
+            "fi_batch_attention_host", "fi_batch_attention_host_async", "fi_host_step_wait",
+            "fi_page_table_step", "fi_append_paged_kv"]
 
 
 class FiError(RuntimeError):
@@ -113,6 +118,10 @@ def lib():
     L.fi_batch_attention_host_async.argtypes = (L.fi_batch_attention_host.argtypes +
                                                 [ctypes.POINTER(ctypes.c_uint64)])
     L.fi_host_step_wait.argtypes = [ctypes.c_uint64]
+    L.fi_page_table_step.argtypes = [_I32, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _I32, _P, _P,
+                                     _P, _P, _I32, _P, _P, _P, _P, _I32, _P, ctypes.c_size_t, _P]
+    L.fi_append_paged_kv.argtypes = [_I32, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _P, _I32, _I32,
+                                     _I64, _I32, _I32, _P, _P, _P, ctypes.c_size_t, _P]
     for name in EXPORTED:
         if name not in ("fi_status_string", "fi_last_error_string"):
             getattr(L, name).restype = _I32
@@ -226,7 +235,8 @@ def fi_batch_decode_paged(plan: Plan, q, k_cache, v_cache, kv_layout, page_strid
                           num_pages, page_indptr_d, page_indices_d, last_page_len_d, sm_scale,
                           k_scale, v_scale, out, lse, workspace, workspace_bytes=None,
                           stream=None, k_head_scale=None, v_head_scale=None):
-    """k_head_scale / v_head_scale: device fp32 [num_kv_heads] or None."""
+    """k_head_scale / v_head_scale: device fp32 [num_kv_heads] or None; for an
+    FI_DTYPE_E4M3_PAGE plan the page scales, [num_pages][num_kv_heads]."""
     wsb = plan.workspace_bytes if workspace_bytes is None else workspace_bytes
     st = lib().fi_batch_decode_paged(plan.handle, _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                      int(kv_layout), int(page_stride_elems), int(num_pages),
@@ -293,6 +303,39 @@ def fi_batch_attention_host_async(plan: Plan, q_h, qo_indptr_h, k_cache, v_cache
 
 def fi_host_step_wait(ticket: int):
     _check(lib().fi_host_step_wait(int(ticket)), "fi_host_step_wait")
+
+
+def fi_page_table_step(batch, slots, new_len, max_requests, max_pages, page_size, kv_len,
+                       kv_len_out, block_table, free_ring, ring_capacity, ring_state,
+                       ring_state_out, page_indptr, page_indices, page_capacity, last_page_len,
+                       qo_indptr, slot_map, positions, token_capacity, workspace,
+                       workspace_bytes=FI_STEP_WORKSPACE_BYTES, stream=None):
+    """All arrays on the device: int32, slot_map int64; slots and positions may
+    be None. The workspace is zero-filled before its first use."""
+    st = lib().fi_page_table_step(int(batch), _ptr(slots), _ptr(new_len), int(max_requests),
+                                  int(max_pages), int(page_size), _ptr(kv_len), _ptr(kv_len_out),
+                                  _ptr(block_table), _ptr(free_ring), int(ring_capacity),
+                                  _ptr(ring_state), _ptr(ring_state_out), _ptr(page_indptr),
+                                  _ptr(page_indices), int(page_capacity), _ptr(last_page_len),
+                                  _ptr(qo_indptr), _ptr(slot_map), _ptr(positions),
+                                  int(token_capacity), _ptr(workspace), int(workspace_bytes),
+                                  _stream(stream))
+    _check(st, "fi_page_table_step")
+
+
+def fi_append_paged_kv(num_tokens, slot_map, k_new, v_new, token_stride_elems, dtype, num_kv_heads,
+                       head_dim, k_cache, v_cache, kv_dtype, kv_layout, page_stride_elems,
+                       num_pages, page_size, k_page_scale, v_page_scale, workspace,
+                       workspace_bytes=FI_STEP_WORKSPACE_BYTES, stream=None):
+    """k_page_scale / v_page_scale: device fp32 [num_pages][num_kv_heads] for an
+    FI_DTYPE_E4M3_PAGE cache, else None."""
+    st = lib().fi_append_paged_kv(int(num_tokens), _ptr(slot_map), _ptr(k_new), _ptr(v_new),
+                                  int(token_stride_elems), int(dtype), int(num_kv_heads),
+                                  int(head_dim), _ptr(k_cache), _ptr(v_cache), int(kv_dtype),
+                                  int(kv_layout), int(page_stride_elems), int(num_pages),
+                                  int(page_size), _ptr(k_page_scale), _ptr(v_page_scale),
+                                  _ptr(workspace), int(workspace_bytes), _stream(stream))
+    _check(st, "fi_append_paged_kv")
 
 
 def fi_merge_states(v, s, n, S, H, d, out_dtype, out, lse_out, stream=None):

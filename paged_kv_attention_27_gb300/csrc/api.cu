@@ -7,6 +7,7 @@
 
 #include <atomic>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <new>
 #include <string>
@@ -253,7 +254,9 @@ CUtensorMapDataType tma_type(int dtype) {
   return dtype == FI_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 }
 
-int elem_bytes(int dtype) { return dtype == FI_DTYPE_E4M3 ? 1 : 2; }
+int elem_bytes(int dtype) {
+  return dtype == FI_DTYPE_E4M3 || dtype == FI_DTYPE_E4M3_PAGE ? 1 : 2;
+}
 
 fi_status make_kv_map(CUtensorMap* map, const void* base, int layout, int num_pages, int P,
                       int Hkv, int d, int64_t page_stride, int dtype) {
@@ -903,6 +906,120 @@ fi_status fi_merge_states(const float* v, const float* s, int32_t n, int32_t S, 
   return FI_OK;
 }
 
+fi_status fi_page_table_step(int32_t batch, const int32_t* slots, const int32_t* new_len,
+                             int32_t max_requests, int32_t max_pages, int32_t page_size,
+                             const int32_t* kv_len, int32_t* kv_len_out, int32_t* block_table,
+                             int32_t* free_ring, int32_t ring_capacity,
+                             const int32_t* ring_state, int32_t* ring_state_out,
+                             int32_t* page_indptr, int32_t* page_indices, int32_t page_capacity,
+                             int32_t* last_page_len, int32_t* qo_indptr, int64_t* slot_map,
+                             int32_t* positions, int32_t token_capacity, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (batch < 0 || batch > fi::kStepMaxBatch || max_requests < 1 ||
+      max_requests > fi::kStepMaxRequests || max_pages < 1 || page_size < 1 ||
+      page_size > fi::kStepMaxPageSize || ring_capacity < 1 || page_capacity < 0 ||
+      token_capacity < 0)
+    return FI_ERR_INVALID_ARG;
+  if (batch == 0) return FI_OK;
+  if (!new_len || !kv_len || !kv_len_out || !block_table || !free_ring || !ring_state ||
+      !ring_state_out || !page_indptr || !last_page_len || !qo_indptr || !workspace ||
+      (page_capacity > 0 && !page_indices) || (token_capacity > 0 && !slot_map))
+    return FI_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)slots, (const void*)new_len, (const void*)kv_len,
+                        (const void*)kv_len_out, (const void*)block_table, (const void*)free_ring,
+                        (const void*)ring_state, (const void*)ring_state_out,
+                        (const void*)page_indptr, (const void*)page_indices,
+                        (const void*)last_page_len, (const void*)qo_indptr,
+                        (const void*)positions})
+    if (!aligned(p, 4)) return FI_ERR_INVALID_ARG;
+  if (!aligned(slot_map, 8) || !aligned(workspace, 256)) return FI_ERR_INVALID_ARG;
+  if (workspace_bytes < FI_STEP_WORKSPACE_BYTES) return FI_ERR_WORKSPACE_TOO_SMALL;
+  const fi_status st = check_device();
+  if (st != FI_OK) return st;
+  fi::PageStepParams p;
+  p.batch = batch;
+  p.slots = slots;
+  p.new_len = new_len;
+  p.max_requests = max_requests;
+  p.max_pages = max_pages;
+  p.page_size = page_size;
+  p.kv_len = kv_len;
+  p.kv_len_out = kv_len_out;
+  p.block_table = block_table;
+  p.free_ring = free_ring;
+  p.ring_capacity = ring_capacity;
+  p.ring_state = ring_state;
+  p.ring_state_out = ring_state_out;
+  p.page_indptr = page_indptr;
+  p.page_indices = page_indices;
+  p.page_capacity = page_capacity;
+  p.last_page_len = last_page_len;
+  p.qo_indptr = qo_indptr;
+  p.slot_map = slot_map;
+  p.positions = positions;
+  p.token_capacity = token_capacity;
+  p.err = static_cast<uint32_t*>(workspace);
+  p.ticket = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + fi::kStepTicketOffset);
+  const cudaError_t e = fi::launch_page_step(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FI_OK : cuda_fail(e, "page-table step launch");
+}
+
+fi_status fi_append_paged_kv(int32_t num_tokens, const int64_t* slot_map, const void* k_new,
+                             const void* v_new, int64_t token_stride_elems, int32_t dtype,
+                             int32_t num_kv_heads, int32_t head_dim, void* k_cache,
+                             void* v_cache, int32_t kv_dtype, int32_t kv_layout,
+                             int64_t page_stride_elems, int32_t num_pages, int32_t page_size,
+                             float* k_page_scale, float* v_page_scale, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (num_tokens < 0 || num_kv_heads <= 0 || head_dim <= 0 || page_size <= 0 || num_pages < 0 ||
+      (dtype != FI_DTYPE_BF16 && dtype != FI_DTYPE_FP16) ||
+      (kv_layout != FI_LAYOUT_NHD && kv_layout != FI_LAYOUT_HND))
+    return FI_ERR_INVALID_ARG;
+  if (kv_dtype == FI_DTYPE_E4M3) return FI_ERR_UNSUPPORTED;
+  if (kv_dtype != dtype && kv_dtype != FI_DTYPE_E4M3_PAGE) return FI_ERR_INVALID_ARG;
+  if ((head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+      (page_size != 16 && page_size != 32) || num_kv_heads > 65535 / 2)
+    return FI_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return FI_OK;
+  const bool page_scales = kv_dtype == FI_DTYPE_E4M3_PAGE;
+  const int64_t row = int64_t(num_kv_heads) * head_dim, page = row * page_size;
+  if (token_stride_elems == 0) token_stride_elems = row;
+  if (page_stride_elems == 0) page_stride_elems = page;
+  if (token_stride_elems < row || token_stride_elems % 8 != 0 || page_stride_elems < page ||
+      page_stride_elems % (16 / elem_bytes(kv_dtype)) != 0)
+    return FI_ERR_INVALID_ARG;
+  if (!slot_map || !k_new || !v_new || !k_cache || !v_cache || !workspace ||
+      (page_scales && (!k_page_scale || !v_page_scale)))
+    return FI_ERR_INVALID_ARG;
+  if (!aligned(slot_map, 8) || !aligned(k_new, 16) || !aligned(v_new, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(workspace, 256) ||
+      (page_scales && (!aligned(k_page_scale, 4) || !aligned(v_page_scale, 4))))
+    return FI_ERR_INVALID_ARG;
+  if (workspace_bytes < FI_STEP_WORKSPACE_BYTES) return FI_ERR_WORKSPACE_TOO_SMALL;
+  const fi_status st = check_device();
+  if (st != FI_OK) return st;
+  fi::AppendParams p;
+  p.num_tokens = num_tokens;
+  p.slot_map = slot_map;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.token_stride = token_stride_elems;
+  p.num_kv_heads = num_kv_heads;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.page_stride = page_stride_elems;
+  p.slot_stride = kv_layout == FI_LAYOUT_NHD ? row : head_dim;
+  p.head_stride = kv_layout == FI_LAYOUT_NHD ? head_dim : int64_t(page_size) * head_dim;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.k_scale = k_page_scale;
+  p.v_scale = v_page_scale;
+  p.err = static_cast<uint32_t*>(workspace);
+  const cudaError_t e =
+      fi::launch_append(head_dim, dtype, kv_dtype, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FI_OK : cuda_fail(e, "append launch");
+}
+
 fi_status fi_check_device_status(void* workspace, void* stream_ptr) {
   if (!workspace) return FI_ERR_INVALID_ARG;
   fi_status st = check_device();
@@ -915,6 +1032,7 @@ fi_status fi_check_device_status(void* workspace, void* stream_ptr) {
   if (e != cudaSuccess) return cuda_fail(e, "device status read");
   if (word & fi::kErrTimeout) return FI_ERR_DEVICE_TIMEOUT;
   if (word & fi::kErrBounds) return FI_ERR_DEVICE_BOUNDS;
+  if (word & fi::kErrPages) return FI_ERR_OUT_OF_PAGES;
   return FI_OK;
 }
 
@@ -928,6 +1046,7 @@ const char* fi_status_string(fi_status status) {
     case FI_ERR_DEVICE_TIMEOUT: return "device wait timed out";
     case FI_ERR_DEVICE_BOUNDS: return "page index outside the cache";
     case FI_ERR_NO_DEVICE: return "no CUDA device";
+    case FI_ERR_OUT_OF_PAGES: return "not enough free pages";
   }
   return "unknown status";
 }

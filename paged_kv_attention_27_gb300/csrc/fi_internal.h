@@ -57,6 +57,14 @@ constexpr size_t kAlign = 256;
 // Error bits in the first word of the workspace.
 constexpr uint32_t kErrTimeout = 1u;
 constexpr uint32_t kErrBounds = 2u;
+constexpr uint32_t kErrPages = 4u;
+
+// Step workspace (fi_page_table_step, fi_append_paged_kv): the error word, and
+// the ticket counter of fi_page_table_step's blocks at this offset.
+constexpr size_t kStepTicketOffset = 64;
+constexpr int32_t kStepMaxBatch = 8192;
+constexpr int32_t kStepMaxRequests = 262144;
+constexpr int32_t kStepMaxPageSize = 1024;
 
 inline int decode_tile_tokens(int head_dim) { return 8192 / head_dim; }  // 32 KB of K+V
 // A batch with both decode rows and multi-row (chunked prefill) requests runs
