@@ -22,7 +22,8 @@ LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libfi.so")
 
 SOURCES = ["plan.cpp", "api.cu", "decode.cu", "merge.cu", "prefill.cu", "prefill_pair.cu",
-           "noalloc.cu", "page_step.cu", "append.cu"]
+           "noalloc.cu", "page_step.cu", "append.cu",
+           "decode_page8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -245,17 +245,19 @@ fi_status upload_image_static(void* dst, const fi::Plan& P, cudaStream_t stream)
   return e == cudaSuccess ? FI_OK : cuda_fail(e, "work-list upload");
 }
 
+int elem_bytes(int dtype) {
+  return dtype == FI_DTYPE_E4M3 || dtype == FI_DTYPE_E4M3_PAGE ? 1 : 2;
+}
+
 // Tensor map over a paged K or V cache that fetches one (page, kv head)
 // block per box: page_size rows x 64 dims (128 bytes, 128-byte swizzled)
 // for a 16-bit cache; page_size whole rows of head_dim bytes for an FP8
-// cache (128-byte swizzled at head_dim 128, unswizzled otherwise).
+// cache (128-byte swizzled at head_dim 128, unswizzled otherwise). A
+// page-scaled FP8 cache: page_size rows x 128 bytes, 128-byte swizzled, or at
+// head_dim 64 x 64 bytes, 64-byte swizzled (MMA operands as they arrive).
 CUtensorMapDataType tma_type(int dtype) {
-  if (dtype == FI_DTYPE_E4M3) return CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if (elem_bytes(dtype) == 1) return CU_TENSOR_MAP_DATA_TYPE_UINT8;
   return dtype == FI_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-}
-
-int elem_bytes(int dtype) {
-  return dtype == FI_DTYPE_E4M3 || dtype == FI_DTYPE_E4M3_PAGE ? 1 : 2;
 }
 
 fi_status make_kv_map(CUtensorMap* map, const void* base, int layout, int num_pages, int P,
@@ -270,7 +272,9 @@ fi_status make_kv_map(CUtensorMap* map, const void* base, int layout, int num_pa
   cuuint32_t box[4];
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const cuuint64_t eb = cuuint64_t(elem_bytes(dtype));
-  const cuuint32_t inner = dtype == FI_DTYPE_E4M3 ? cuuint32_t(d) : 64u;
+  const bool page8 = dtype == FI_DTYPE_E4M3_PAGE;
+  const cuuint32_t inner = page8 ? cuuint32_t(d < 128 ? d : 128)
+                                 : dtype == FI_DTYPE_E4M3 ? cuuint32_t(d) : 64u;
   if (layout == FI_LAYOUT_NHD) {
     dims[0] = d; dims[1] = Hkv; dims[2] = P; dims[3] = num_pages;
     strides[0] = cuuint64_t(d) * eb;
@@ -285,7 +289,8 @@ fi_status make_kv_map(CUtensorMap* map, const void* base, int layout, int num_pa
   strides[2] = cuuint64_t(page_stride) * eb;
   // FP8 rows of 128 bytes are swizzled too (the decode kernel reads MMA
   // fragments from them); other FP8 row lengths are not
-  const CUtensorMapSwizzle swizzle = (dtype != FI_DTYPE_E4M3 || d == 128)
+  const CUtensorMapSwizzle swizzle = (page8 && d == 64) ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : (dtype != FI_DTYPE_E4M3 || d == 128)
                                          ? CU_TENSOR_MAP_SWIZZLE_128B
                                          : CU_TENSOR_MAP_SWIZZLE_NONE;
   CUresult r = enc(map, tma_type(dtype), 4, const_cast<void*>(base), dims,
@@ -429,6 +434,8 @@ fi_status run_paged(fi_plan_t plan, bool prefill_call, const void* q, const int3
       !aligned(workspace, 256) || (lse && !aligned(lse, 4)) ||
       (k_head_scale && !aligned(k_head_scale, 4)) || (v_head_scale && !aligned(v_head_scale, 4)))
     return FI_ERR_INVALID_ARG;
+  const bool page8 = P.kv_dtype == FI_DTYPE_E4M3_PAGE;   // page scales are required
+  if (page8 && (!k_head_scale || !v_head_scale)) return FI_ERR_INVALID_ARG;
   fi_status st = check_run_scalars(P, kv_layout, page_stride_elems, sm_scale, k_scale, v_scale);
   if (st != FI_OK) return st;
   const int64_t page_elems = int64_t(P.page_size) * P.num_kv_heads * P.head_dim;
@@ -472,11 +479,12 @@ fi_status run_paged(fi_plan_t plan, bool prefill_call, const void* q, const int3
 
   CUtensorMap qmap;
   if (!P.prefill_items.empty() || !P.prefix_items.empty()) {
-    // prefill tiles hold 128 rows of one head; shared-prefix tiles 128 / g
-    // rows of the g heads of a kv head (a decode plan has only the latter)
+    // prefill tiles hold 128 rows of one head; shared-prefix tiles, and all
+    // tiles over a page-scaled cache, 128 / g rows of the g heads of a kv
+    // head (a decode plan has only the former of these)
     st = q_map(&qmap, q, P.total_q, P.num_qo_heads,
-                    P.prefix_items.empty() ? 1 : P.num_qo_heads / P.num_kv_heads, P.head_dim,
-                    P.dtype);
+                    P.prefix_items.empty() && !page8 ? 1 : P.num_qo_heads / P.num_kv_heads,
+                    P.head_dim, P.dtype);
     if (st != FI_OK) return st;
   }
 
@@ -621,8 +629,10 @@ fi_status run_paged(fi_plan_t plan, bool prefill_call, const void* q, const int3
       if (e != cudaSuccess) return cuda_fail(e, "shared-prefix launch");
     }
     if (!P.decode_items.empty()) {
-      e = fi::launch_decode(P.head_dim, group, P.dtype, P.kv_dtype, kmap, vmap, dp,
-                            int(P.decode_items.size()), P.num_sms, dstream);
+      e = page8 ? fi::launch_decode_page8(P.head_dim, group, P.dtype, kmap, vmap, dp,
+                                          int(P.decode_items.size()), P.num_sms, dstream)
+                : fi::launch_decode(P.head_dim, group, P.dtype, P.kv_dtype, kmap, vmap, dp,
+                                    int(P.decode_items.size()), P.num_sms, dstream);
       if (e != cudaSuccess) return cuda_fail(e, "decode launch");
     }
     if (both) {

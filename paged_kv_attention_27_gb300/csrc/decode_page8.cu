@@ -1,0 +1,757 @@
+// Batch decode over a page-scaled FP8 cache: out = softmax(sm_scale q K^T) V
+// with K = s_k(page, head) * codes and V = s_v(page, head) * codes.
+//
+// A work item is (request, kv head, chunk of keys); the g query heads of the
+// kv head share every page that is loaded. HBM-bound: 2 bytes per key and
+// dimension for K and V together against 4 g flops, so an SM has about 1400
+// cycles per 32 KB tile of 128 keys (head_dim 128) and may not spend
+// instructions per byte. Hence both products run on tcgen05 with the cache
+// bytes as they arrive, nothing is converted, and the roles of rows and
+// columns are swapped against prefill: keys (or dimensions) are the 128 M
+// rows, heads the N columns.
+//   S[key][head]  = K (A, K-major, e4m3) x Q^T (B, e4m3)
+//   O[dim][head] += V^T (A, MN-major, e4m3) x P^T (B, e4m3)
+// The 16-bit q and the fp32 weights enter as sums of e4m3 terms, each in its
+// own column: x = t0 + t1 / 16 (+ t2 / 256), t0 = e4m3(x), t1 = e4m3(16 (x -
+// t0)), ... Two terms carry the 8 significand bits of bf16, three the 11 of
+// fp16: q (times a power of two that puts its largest element at 224..448)
+// enters exactly, and weights are rounded as bf16 (fp16) weights would be. N
+// is at least 16 for M = 128, so up to 8 heads x 2 terms cost nothing extra.
+//
+// Scales: the score of a key is multiplied by its page's s_k with the softmax
+// scale. A weight is multiplied by its page's s_v before it is rounded, p s_v
+// = 2^(s + log2 s_v), with a running maximum of its own: sums of p (the
+// denominator and lse) and of p s_v v then both keep their leading bits, for
+// any spread of the pages' scales.
+//
+// Roles (6 warps): 0-3 softmax (thread = key of the tile = TMEM lane), then
+// the epilogue (thread = dimension); 4 copies pages by TMA and page scales by
+// cp.async into a ring; 5 issues the MMAs (the scores of tile j + 1 before the
+// output of tile j, with two score buffers). The launch is persistent: a CTA
+// takes items from a counter and the ring runs on from item to item.
+#include <cfloat>
+#include <type_traits>
+
+#include "elem.cuh"
+#include "fi_internal.h"
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace fi {
+
+namespace {
+
+using namespace dev;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kItemRing = 8;
+// A weight is at most 2^kGrow above the running maximum (the maximum moves
+// when a score passes it by more), and is stored times 2^kWeightExp: at most
+// 256, below E4M3's 448.
+constexpr float kGrow = 1.f;
+constexpr float kWeightUnit = 128.f;
+
+template <int D, int G, class E>
+struct D8Cfg {
+  static constexpr int T = kPage8DecodeTile;                // keys per tile
+  static constexpr int TERMS = std::is_same<E, Bf16>::value ? 2 : 3;
+  static constexpr int COLS = G * TERMS;                    // column term * G + head
+  static constexpr int N = COLS <= 16 ? 16 : 32;
+  static constexpr int ROWB = D < 128 ? D : 128;            // bytes of a shared-memory row
+  static constexpr int DB = D <= 128 ? 1 : D / 128;         // 128-byte slices of a key
+  static constexpr uint32_t SWZ = ROWB == 128 ? 2 : 4;      // 128- or 64-byte swizzle
+  static constexpr uint32_t ATOM = 8 * ROWB;
+  static constexpr int KBYTES = T * D;                      // one K (or V) tile
+  static constexpr int STAGE = 2 * KBYTES;
+  static constexpr int CTAS = D <= 128 ? 2 : 1;             // per SM
+  static constexpr int NST = D == 64 ? 6 : 3;
+  static constexpr int QBYTES = N * D;
+  static constexpr int PBYTES = T * N;
+  static constexpr int OFF_Q = NST * STAGE;                 // two buffers
+  static constexpr int OFF_P = OFF_Q + 2 * QBYTES;          // two buffers
+  static constexpr int SMEM = OFF_P + 2 * PBYTES + 1024;
+  static constexpr int THREADS = 192;
+  static constexpr uint32_t TMEM_COLS = N * (2 + DB) <= 64 ? 64 : 128;
+  static constexpr uint32_t IDESC_S = idesc_e4m3(128, N, 0, 0);
+  static constexpr uint32_t IDESC_O = idesc_e4m3(128, 16, 1, 1);
+  static constexpr int DPL = D / 32;                        // q elements per lane and head
+  static_assert(SMEM * CTAS <= 227 * 1024, "shared-memory budget");
+  static_assert(COLS <= 32 && N * (2 + DB) <= 128, "");
+};
+
+struct D8Barriers {
+  uint64_t item_full[kItemRing], item_empty[kItemRing];
+  uint64_t k_full[6], v_full[6], empty[6];
+  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t drain;
+};
+
+// A float in [0, inf) orders as its bits.
+__device__ __forceinline__ float warp_max(float x) {
+  int k = __float_as_int(x);
+  k = k < 0 ? k ^ 0x7fffffff : k;
+  k = __reduce_max_sync(0xffffffffu, k);
+  return __int_as_float(k < 0 ? k ^ 0x7fffffff : k);
+}
+
+__device__ __forceinline__ float pow2i(int k) { return __uint_as_float(uint32_t(127 + k) << 23); }
+
+__device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+}
+
+template <int D, int G, class E>
+__global__ void __launch_bounds__(D8Cfg<D, G, E>::THREADS, D8Cfg<D, G, E>::CTAS)
+decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
+                    const __grid_constant__ CUtensorMap v_map, DecodeParams prm) {
+  using C = D8Cfg<D, G, E>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) D8Barriers bars;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_flag;
+  __shared__ int item_ring[kItemRing];
+  __shared__ __align__(8) float2 scale_sh[C::NST][8];   // per page of a tile: s_k (-1: no page), s_v
+  __shared__ float q_unit[2][G];                        // score scale of a head, by item parity
+  __shared__ float red[4][2 * G];
+  __shared__ int merge_last;
+
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* gen = smem_raw + (base - smem_u32(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t limit = prm.wait_limit_ns;
+  const int P = prm.page_size, ppt = C::T / P;
+  const int hkv = prm.num_qo_heads / G;
+
+  auto item_at = [&](int n, int& idx) {
+    if (!mbar_wait_bounded(smem_u32(&bars.item_full[n % kItemRing]), (n / kItemRing) & 1, limit,
+                           &abort_flag))
+      return false;
+    idx = *reinterpret_cast<volatile int*>(&item_ring[n % kItemRing]);
+    return true;
+  };
+  auto item_done = [&](int n) { mbar_arrive(smem_u32(&bars.item_empty[n % kItemRing])); };
+  // tiles of an item: its keys from the start of its first page
+  auto lead_of = [&](const WorkItem& w) { return w.tok_begin % P; };
+  auto tiles_of = [&](const WorkItem& w) {
+    const int n = w.tok_end - w.tok_begin;
+    return n > 0 ? (n + lead_of(w) + C::T - 1) / C::T : 0;
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kItemRing; ++s) {
+      mbar_init(smem_u32(&bars.item_full[s]), 1);
+      mbar_init(smem_u32(&bars.item_empty[s]), 5);      // 4 softmax warps, the MMA warp
+    }
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(smem_u32(&bars.k_full[s]), 1 + ppt);    // K's bytes, and each page's scales
+      mbar_init(smem_u32(&bars.v_full[s]), 1);
+      mbar_init(smem_u32(&bars.empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&bars.q_full[s]), 4);
+      mbar_init(smem_u32(&bars.s_full[s]), 1);
+      mbar_init(smem_u32(&bars.p_full[s]), 4);
+      mbar_init(smem_u32(&bars.pv_done[s]), 1);
+    }
+    mbar_init(smem_u32(&bars.drain), 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  // rows of Q that no head uses stay zero
+  for (int i = threadIdx.x; i < 2 * C::QBYTES / 16; i += C::THREADS)
+    st_shared_zero16(base + C::OFF_Q + i * 16);
+  fence_proxy_async_smem();
+  if (warp == 5) {
+    tmem_alloc(smem_u32(&tmem_base_sh), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  const uint32_t o_col0 = tmem + 2 * C::N;
+  int issued = 0;   // the producer: tiles whose copies it has issued
+
+  if (warp == 4) {
+    // ---------------------------------------------------------------- producer
+    if (lane == 0) {
+      prefetch_tensormap(&k_map);
+      prefetch_tensormap(&v_map);
+    }
+    const uint32_t box = uint32_t(P) * C::ROWB;
+    auto publish = [&](int n, int value) {
+      if (n >= kItemRing &&
+          !mbar_wait_bounded(smem_u32(&bars.item_empty[n % kItemRing]), ((n / kItemRing) & 1) ^ 1,
+                             limit, &abort_flag))
+        return false;
+      item_ring[n % kItemRing] = value;
+      mbar_arrive(smem_u32(&bars.item_full[n % kItemRing]));
+      return true;
+    };
+    auto next_item = [&](int n, int& idx) {   // item n of this CTA, published
+      int v = -1;
+      bool good = true;
+      if (lane == 0) {
+        v = n == 0 ? int(blockIdx.x) : int(gridDim.x + atomicAdd(prm.work_counter, 1u));
+        if (v >= prm.n_items) v = -1;
+        good = publish(n, v);
+      }
+      idx = __shfl_sync(0xffffffffu, v, 0);
+      return __shfl_sync(0xffffffffu, good, 0) != 0;
+    };
+    auto pages_in = [&](const WorkItem& w, int j) { return min(ppt, w.n_pages - j * ppt); };
+    int it = -1, g = 0;
+    bool ok = next_item(0, it);
+    WorkItem w;
+    if (ok && it >= 0) w = prm.items[it];
+    int next_page = -1;
+    if (ok && it >= 0 && lane < pages_in(w, 0)) next_page = prm.page_indices[w.page_begin + lane];
+    for (int n = 0; ok && it >= 0; ++n) {
+      const int nt = tiles_of(w);
+      const int c1 = prm.layout == FI_LAYOUT_NHD ? w.head : 0;
+      const int c2 = prm.layout == FI_LAYOUT_NHD ? 0 : w.head;
+      int it_next = -1;
+      if (!next_item(n + 1, it_next)) {
+        ok = false;
+        break;
+      }
+      WorkItem wn;
+      if (it_next >= 0) wn = prm.items[it_next];
+      if (nt == 0) {
+        next_page = -1;
+        if (it_next >= 0 && lane < pages_in(wn, 0)) next_page = prm.page_indices[wn.page_begin + lane];
+      }
+      for (int j = 0; j < nt; ++j, ++g) {
+        const int st = g % C::NST;
+        const int page = next_page;
+        const bool mine = lane < pages_in(w, j);
+        const bool valid = mine && page >= 0 && page < prm.num_pages;
+        if (mine && !valid) atomicOr(prm.err, kErrBounds);
+        next_page = -1;
+        if (j + 1 < nt) {
+          if (lane < pages_in(w, j + 1))
+            next_page = prm.page_indices[w.page_begin + (j + 1) * ppt + lane];
+        } else if (it_next >= 0 && lane < pages_in(wn, 0)) {
+          next_page = prm.page_indices[wn.page_begin + lane];
+        }
+        const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, valid))) * C::DB * box;
+        if (g >= C::NST && !mbar_wait_warp(smem_u32(&bars.empty[st]), ((g / C::NST) & 1) ^ 1, limit,
+                                           &abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t kf = smem_u32(&bars.k_full[st]), vf = smem_u32(&bars.v_full[st]);
+        const bool skip = g == 0 && prm.fault_kind == 1 && blockIdx.x == 0;
+        if (lane == 0) {
+          if (!skip) mbar_arrive_expect_tx(kf, bytes);
+          mbar_arrive_expect_tx(vf, bytes);
+        }
+        __syncwarp();
+        if (lane < ppt) {
+          if (valid) {
+            const uint32_t dst = base + st * C::STAGE + lane * box;
+#pragma unroll
+            for (int b = 0; b < C::DB; ++b) {
+              if (!skip) tma_load_4d(dst + b * C::T * C::ROWB, &k_map, kf, b * 128, c1, c2, page);
+            }
+#pragma unroll
+            for (int b = 0; b < C::DB; ++b)
+              tma_load_4d(dst + C::KBYTES + b * C::T * C::ROWB, &v_map, vf, b * 128, c1, c2, page);
+            const size_t at = size_t(page) * hkv + w.head;
+            const uint32_t sc = smem_u32(&scale_sh[st][lane]);
+            cp_async4(sc, prm.k_head_scale + at);
+            cp_async4(sc + 4, prm.v_head_scale + at);
+            cp_async_arrive(kf);
+          } else {
+            scale_sh[st][lane] = make_float2(-1.f, 1.f);
+            mbar_arrive(kf);
+          }
+        }
+        issued = g + 1;
+      }
+      w = wn;
+      it = it_next;
+    }
+    if (!ok && lane == 0) {
+      abort_flag = 1;
+      atomicOr(prm.err, kErrTimeout);
+    }
+    cp_async_wait_all();
+    __syncwarp();
+  } else if (warp == 5) {
+    // -------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint64_t kd0 = sdesc_swz(base, 16, C::ATOM, C::SWZ);
+      // head_dim 64: the second 64 of the 128 M rows repeat the first (their
+      // accumulator rows are not read)
+      const uint64_t vd0 = sdesc_swz(base + C::KBYTES, 0, C::ATOM, C::SWZ);
+      const uint64_t qd0 = sdesc_swz(base + C::OFF_Q, 16, C::ATOM, C::SWZ);
+      const uint64_t pd0 = sdesc_swz(base + C::OFF_P, 128, 128, 0);
+      bool ok = true;
+      int g = 0;
+      auto scores = [&](int q_buf) {     // S of tile g
+        const int st = g % C::NST;
+        if (!mbar_wait_bounded(smem_u32(&bars.k_full[st]), (g / C::NST) & 1, limit, &abort_flag))
+          return false;
+        tc_fence_after();
+        const uint64_t kd = kd0 + uint64_t((st * C::STAGE) >> 4);
+        const uint64_t qd = qd0 + uint64_t((q_buf * C::QBYTES) >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          const int b = k * 32 / 128, o = k * 32 % 128;
+          tc_mma_f8_ss(tmem + (g & 1) * C::N, kd + uint64_t((b * C::T * C::ROWB + o) >> 4),
+                       qd + uint64_t((b * C::N * C::ROWB + o) >> 4), C::IDESC_S, k > 0 ? 1u : 0u);
+        }
+        tc_commit(smem_u32(&bars.s_full[g & 1]));
+        return true;
+      };
+      auto outputs = [&](int t, bool first) {   // O += V^T P^T of tile t
+        const int st = t % C::NST;
+        if (!mbar_wait_bounded(smem_u32(&bars.v_full[st]), (t / C::NST) & 1, limit, &abort_flag) ||
+            !mbar_wait_bounded(smem_u32(&bars.p_full[t & 1]), (t >> 1) & 1, limit, &abort_flag))
+          return false;
+        tc_fence_after();
+        const uint64_t vd = vd0 + uint64_t((st * C::STAGE) >> 4);
+        const uint64_t pd = pd0 + uint64_t(((t & 1) * C::PBYTES) >> 4);
+#pragma unroll
+        for (int b = 0; b < C::DB; ++b)
+#pragma unroll
+          for (int c = 0; c < C::N / 16; ++c)
+#pragma unroll
+            for (int k = 0; k < C::T / 32; ++k)
+              tc_mma_f8_ss(o_col0 + b * C::N + c * 16,
+                           vd + uint64_t((b * C::T * C::ROWB + k * 32 * C::ROWB) >> 4),
+                           pd + uint64_t((c * C::T * 16 + k * 32 * 16) >> 4), C::IDESC_O,
+                           (!first || k > 0) ? 1u : 0u);
+        tc_commit(smem_u32(&bars.empty[st]));
+        tc_commit(smem_u32(&bars.pv_done[t & 1]));
+        return true;
+      };
+      int pending = -1;          // tile whose output MMAs are still to be issued
+      bool pending_first = false;
+      for (int n = 0; ok; ++n) {
+        int it = -1;
+        ok = item_at(n, it);
+        item_done(n);
+        if (!ok || it < 0) break;
+        const int nt = tiles_of(prm.items[it]);
+        // the previous item's last output does not wait for this item's q
+        if (pending >= 0) {
+          ok = outputs(pending, pending_first);
+          pending = -1;
+          if (!ok) break;
+        }
+        ok = mbar_wait_bounded(smem_u32(&bars.q_full[n & 1]), (n >> 1) & 1, limit, &abort_flag);
+        for (int j = 0; ok && j < nt; ++j, ++g) {
+          ok = scores(n & 1);
+          if (ok && pending >= 0) ok = outputs(pending, pending_first);
+          pending = g;
+          pending_first = j == 0;
+        }
+      }
+      if (ok && pending >= 0) ok = outputs(pending, pending_first);
+      if (!ok) {
+        abort_flag = 1;
+        atomicOr(prm.err, kErrTimeout);
+      }
+      // every MMA issued so far completes before the TMEM is released
+      tc_commit(smem_u32(&bars.drain));
+      mbar_wait_bounded(smem_u32(&bars.drain), 0, limit, nullptr);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------ softmax + epilogue
+    const int t = threadIdx.x;                          // key of the tile, then dimension
+    const uint32_t lane_off = uint32_t(warp * 32) << 16;
+    const float scale0 = prm.sm_scale * kLog2e;
+    // The four warps meet at named barriers, so none of them leaves alone: a
+    // wait that runs out sets `ok` to false and the next vote ends all four.
+    bool ok = true;
+    int g = 0;
+    auto sync4 = [] { named_bar_sync(1, 128); };
+    auto all_ok = [&] { return !named_bar_or(1, 128, !ok); };
+    auto wait = [&](uint64_t& bar, uint32_t parity) {
+      const bool good = mbar_wait_warp(smem_u32(&bar), parity, limit, &abort_flag);
+      if (!good) ok = false;
+      return good;
+    };
+    for (int n = 0;; ++n) {
+      int it = -1;
+      if (lane == 0) {
+        ok = item_at(n, it);
+        item_done(n);
+      }
+      it = __shfl_sync(0xffffffffu, it, 0);
+      ok = __shfl_sync(0xffffffffu, ok, 0) != 0;
+      if (!all_ok()) {
+        ok = false;
+        break;
+      }
+      if (it < 0) break;
+      const WorkItem w = prm.items[it];
+      const int nt = tiles_of(w), lead = lead_of(w);
+      // ---- q as e4m3 terms: warp i takes heads i and i + 4
+      if (nt == 0) {
+        if (lane == 0) mbar_arrive(smem_u32(&bars.q_full[n & 1]));
+      } else {
+#pragma unroll
+        for (int h = warp; h < G; h += 4) {
+          const uint16_t* src = reinterpret_cast<const uint16_t*>(prm.q) +
+                                (size_t(w.q_row) * prm.num_qo_heads + w.head * G + h) * D +
+                                lane * C::DPL;
+          float x[C::DPL];
+          if constexpr (C::DPL == 8) {
+            unpack8<E>(*reinterpret_cast<const uint4*>(src), x);
+          } else if constexpr (C::DPL == 4) {
+            const uint2 u = *reinterpret_cast<const uint2*>(src);
+            x[0] = E::lo(u.x); x[1] = E::hi(u.x); x[2] = E::lo(u.y); x[3] = E::hi(u.y);
+          } else {
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(src);
+            x[0] = E::lo(u); x[1] = E::hi(u);
+          }
+          float a = 0.f;
+#pragma unroll
+          for (int e = 0; e < C::DPL; ++e) {
+            const float b = fabsf(x[e]);
+            a = b < INFINITY ? fmaxf(a, b) : a;
+          }
+          a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+          const uint32_t u = __float_as_uint(a);
+          // the smallest k >= -100 with a <= 448 * 2^k
+          const int k = max(int(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+          const float inv = pow2i(-k);
+#pragma unroll
+          for (int e = 0; e < C::DPL; ++e)   // (the conversion saturates infinities: NaN instead)
+            x[e] = fabsf(x[e]) < INFINITY ? x[e] * inv : __uint_as_float(0x7fc00000u);
+          const int off = lane * C::DPL, slice = off / 128, byte = off % C::ROWB;
+#pragma unroll
+          for (int tm = 0; tm < C::TERMS; ++tm) {
+            const int row = tm * G + h;
+            const int sw = C::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
+            uint8_t* dst = gen + C::OFF_Q + (n & 1) * C::QBYTES + slice * C::N * C::ROWB +
+                           row * C::ROWB + (((byte >> 4) ^ sw) << 4) + (byte & 15);
+            uint32_t code[(C::DPL + 3) / 4];
+#pragma unroll
+            for (int e = 0; e < C::DPL; e += 2) {
+              const uint32_t c = E4m3::from_f32x2(x[e], x[e + 1]);
+              const uint32_t f = E4m3::to_f16x2(c);
+              x[e] = (x[e] - Fp16::lo(f)) * 16.f;
+              x[e + 1] = (x[e + 1] - Fp16::hi(f)) * 16.f;
+              if (e % 4 == 0) code[e / 4] = c;
+              else code[e / 4] |= c << 16;
+            }
+            if constexpr (C::DPL == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
+            else if constexpr (C::DPL == 4) *reinterpret_cast<uint32_t*>(dst) = code[0];
+            else *reinterpret_cast<uint16_t*>(dst) = uint16_t(code[0]);
+          }
+          if (lane == 0) q_unit[n & 1][h] = scale0 * pow2i(k);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.q_full[n & 1]));
+        sync4();   // q_unit of every head
+      }
+      float unit[G], m[G], mu[G], l[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        unit[h] = nt > 0 ? q_unit[n & 1][h] : 0.f;
+        m[h] = mu[h] = -INFINITY;
+        l[h] = 0.f;
+      }
+      for (int j = 0; j < nt; ++j, ++g) {
+        const int st = g % C::NST;
+        // this key's page scales
+        wait(bars.k_full[st], (g / C::NST) & 1);
+        const float2 sc = scale_sh[st][t / P];
+        const int i = j * C::T + t - lead;              // key number from tok_begin
+        const bool seen = i >= 0 && i < w.tok_end - w.tok_begin && sc.x >= 0.f;
+        const float lv = lg2(sc.y);
+        wait(bars.s_full[g & 1], (g >> 1) & 1);
+        tc_fence_after();
+        uint32_t r[C::N];
+        if constexpr (C::N == 16) tmem_ld16(tmem + lane_off + (g & 1) * C::N, r);
+        else tmem_ld32(tmem + lane_off + (g & 1) * C::N, r);
+        tmem_wait_ld();
+        float s[G];
+        bool grow = false;
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          float x = __uint_as_float(r[h]);
+          x = fmaf(__uint_as_float(r[G + h]), 0.0625f, x);
+          if (C::TERMS == 3) x = fmaf(__uint_as_float(r[2 * G + h]), 0.00390625f, x);
+          s[h] = seen ? x * (sc.x * unit[h]) : -INFINITY;
+          grow |= s[h] > m[h] + kGrow || s[h] + lv > mu[h] + kGrow;
+        }
+        if (named_bar_or(1, 128, grow || !ok)) {
+          // new maxima over the tile's keys, and O and l on the new scale
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            // (NaN scores leave the maxima alone)
+            const float a = warp_max(s[h] == s[h] ? s[h] : -INFINITY);
+            const float b = warp_max(s[h] + lv == s[h] + lv ? s[h] + lv : -INFINITY);
+            if (lane == 0) {
+              red[warp][h] = a;
+              red[warp][G + h] = b;
+            }
+          }
+          if (!all_ok()) {
+            ok = false;
+            break;
+          }
+          float alpha[G];
+          bool live = false;
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float a = fmaxf(fmaxf(red[0][h], red[1][h]), fmaxf(red[2][h], red[3][h]));
+            const float b = fmaxf(fmaxf(red[0][G + h], red[1][G + h]),
+                                  fmaxf(red[2][G + h], red[3][G + h]));
+            const float m2 = fmaxf(m[h], a), mu2 = fmaxf(mu[h], b);
+            l[h] *= m[h] == -INFINITY ? 0.f : ex2(m[h] - m2);
+            alpha[h] = mu[h] == -INFINITY ? 0.f : ex2(mu[h] - mu2);
+            live |= alpha[h] != 1.f;
+            m[h] = m2;
+            mu[h] = mu2;
+          }
+          if (j > 0 && live) {
+            wait(bars.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < C::DB; ++b) {
+              uint32_t o[C::N];
+              const uint32_t at = o_col0 + lane_off + b * C::N;
+              if constexpr (C::N == 16) tmem_ld16(at, o);
+              else tmem_ld32(at, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < C::COLS; ++c)
+                o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[c % G]);
+              if constexpr (C::N == 16) tmem_st16(at, o);
+              else tmem_st32(at, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        // weights: p = 2^(s - m) into the sums, p s_v as e4m3 terms into P^T
+        uint32_t pw[C::N / 4];
+#pragma unroll
+        for (int c = 0; c < C::N / 4; ++c) pw[c] = 0u;
+#pragma unroll
+        for (int h = 0; h < G; h += 2) {
+          float x[2] = {0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < 2 && h + e < G; ++e) {
+            l[h + e] += ex2(s[h + e] - (m[h + e] == -INFINITY ? 0.f : m[h + e]));
+            x[e] = kWeightUnit * ex2(s[h + e] + lv - (mu[h + e] == -INFINITY ? 0.f : mu[h + e]));
+          }
+#pragma unroll
+          for (int tm = 0; tm < C::TERMS; ++tm) {
+            uint32_t c = E4m3::from_f32x2(x[0], x[1]);
+            if (tm + 1 < C::TERMS) {
+              const uint32_t f = E4m3::to_f16x2(c);
+              x[0] = (x[0] - Fp16::lo(f)) * 16.f;
+              x[1] = (x[1] - Fp16::hi(f)) * 16.f;
+            }
+            if (G == 1) c &= 0xffu;
+            const int at = tm * G + h;
+            pw[at / 4] |= c << (8 * (at % 4));
+          }
+        }
+        // P^T: per key 16 bytes of each block of 16 columns; its buffer was
+        // last read by the output MMAs of tile g - 2
+        if (g >= 2) wait(bars.pv_done[g & 1], ((g - 2) >> 1) & 1);
+        uint8_t* pb = gen + C::OFF_P + (g & 1) * C::PBYTES + t * 16;
+#pragma unroll
+        for (int c = 0; c < C::N / 16; ++c)
+          *reinterpret_cast<uint4*>(pb + c * C::T * 16) =
+              make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
+        // V rows of keys outside the item hold stale bytes, maybe NaN codes,
+        // which a zero weight would not cancel
+        if (__any_sync(0xffffffffu, !seen)) {
+          if (wait(bars.v_full[st], (g / C::NST) & 1) && !seen) {
+#pragma unroll
+            for (int b = 0; b < C::DB; ++b)
+#pragma unroll
+              for (int c = 0; c < C::ROWB / 16; ++c)
+                st_shared_zero16(base + st * C::STAGE + C::KBYTES + (b * C::T + t) * C::ROWB + c * 16);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[g & 1]));
+      }
+      // ---- epilogue: out = O 2^(mu - m) / (unit sum p), lse = ln 2 (m + log2 sum p)
+      if (ok && nt > 0) wait(bars.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+      if (!all_ok()) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
+        if (lane == 0) red[warp][h] = l[h];
+      }
+      sync4();
+      float f[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        l[h] = (red[0][h] + red[1][h]) + (red[2][h] + red[3][h]);
+        // (a NaN sum, from a NaN in q or in the cache, stays one)
+        f[h] = l[h] == 0.f ? 0.f
+                           : prm.v_scale * ex2(mu[h] == -INFINITY ? 0.f : mu[h] - m[h]) /
+                                 (kWeightUnit * l[h]);
+      }
+      const bool split = w.slot >= 0;
+      const size_t orow = size_t(split ? w.slot : w.q_row) * prm.num_qo_heads + w.head * G;
+#pragma unroll
+      for (int b = 0; b < C::DB; ++b) {
+        uint32_t o[C::N];
+        if (nt > 0) {
+          const uint32_t at = o_col0 + lane_off + b * C::N;
+          if constexpr (C::N == 16) tmem_ld16(at, o);
+          else tmem_ld32(at, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int c = 0; c < C::N; ++c) o[c] = 0u;
+        }
+        if (t < D) {
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            float x = __uint_as_float(o[h]);
+            x = fmaf(__uint_as_float(o[G + h]), 0.0625f, x);
+            if (C::TERMS == 3) x = fmaf(__uint_as_float(o[2 * G + h]), 0.00390625f, x);
+            x *= f[h];
+            const size_t at = (orow + h) * D + b * 128 + t;
+            if (split) prm.partial_o[at] = x;
+            else reinterpret_cast<uint16_t*>(prm.out)[at] = E::one(x);
+          }
+        }
+      }
+      float* lse = split ? prm.partial_lse : prm.lse;
+      if (lse) {
+#pragma unroll
+        for (int h = 0; h < G; ++h)
+          if (t == h) lse[orow + h] = l[h] == 0.f ? -INFINITY : (m[h] + lg2(l[h])) * kLn2;
+      }
+      tc_fence_before();
+      sync4();   // red is free again
+      if (split) {
+        // the CTA that finishes a row's last chunk merges its states, in slot order
+        const MergeTask mt = prm.merges[w.merge];
+        __threadfence();
+        sync4();
+        if (t == 0) {
+          merge_last = atomicAdd(&prm.merge_counters[w.merge * hkv + w.head], 1u) ==
+                       uint32_t(mt.n_states - 1);
+          if (merge_last) __threadfence();
+        }
+        sync4();
+        if (*reinterpret_cast<volatile int*>(&merge_last)) {
+          const size_t row = size_t(mt.out_row) * prm.num_qo_heads + w.head * G;
+          for (int h = 0; h < G; ++h) {
+            const size_t s0 = size_t(mt.slot_base) * prm.num_qo_heads + w.head * G + h;
+            float top = -INFINITY;
+            for (int i = 0; i < mt.n_states; ++i)
+              top = fmaxf(top, __ldcg(&prm.partial_lse[s0 + size_t(i) * prm.num_qo_heads]));
+            float sum = 0.f, acc[C::DB];
+#pragma unroll
+            for (int b = 0; b < C::DB; ++b) acc[b] = 0.f;
+            for (int i = 0; top != -INFINITY && i < mt.n_states; ++i) {
+              const size_t at = s0 + size_t(i) * prm.num_qo_heads;
+              const float wgt = ex2((__ldcg(&prm.partial_lse[at]) - top) * kLog2e);
+              sum += wgt;
+#pragma unroll
+              for (int b = 0; b < C::DB; ++b)
+                if (t < D) acc[b] = fmaf(wgt, __ldcg(&prm.partial_o[at * D + b * 128 + t]), acc[b]);
+            }
+#pragma unroll
+            for (int b = 0; b < C::DB; ++b)
+              if (t < D)
+                reinterpret_cast<uint16_t*>(prm.out)[(row + h) * D + b * 128 + t] =
+                    E::one(sum == 0.f ? 0.f : acc[b] / sum);
+            if (t == 0 && prm.lse)
+              prm.lse[row + h] = sum == 0.f ? -INFINITY : top + lg2(sum) * kLn2;
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      abort_flag = 1;
+      atomicOr(prm.err, kErrTimeout);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+  // every copy that was issued lands before the CTA exits, also after a timeout
+  if (warp == 4 && lane == 0) {
+    for (int j = max(0, issued - C::NST); j < issued; ++j) {
+      if (!(j == 0 && prm.fault_kind == 1 && blockIdx.x == 0))   // K never issued
+        mbar_wait_bounded(smem_u32(&bars.k_full[j % C::NST]), (j / C::NST) & 1, limit, nullptr);
+      mbar_wait_bounded(smem_u32(&bars.v_full[j % C::NST]), (j / C::NST) & 1, limit, nullptr);
+    }
+  }
+}
+
+template <int D, int G, class E>
+cudaError_t launch_t(const CUtensorMap& km, const CUtensorMap& vm, const DecodeParams& p,
+                     int n_items, int num_sms, cudaStream_t stream) {
+  using C = D8Cfg<D, G, E>;
+  auto kern = decode_page8_kernel<D, G, E>;
+  static std::atomic<uint64_t> configured{0};
+  const cudaError_t e = once_per_device(configured, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  });
+  if (e != cudaSuccess) return e;
+  DecodeParams q = p;
+  q.n_items = n_items;
+  const long long slots = (long long)num_sms * C::CTAS;
+  kern<<<int(slots < n_items ? slots : n_items), C::THREADS, C::SMEM, stream>>>(km, vm, q);
+  return cudaGetLastError();
+}
+
+template <int D, class E>
+cudaError_t launch_g(int group, const CUtensorMap& km, const CUtensorMap& vm,
+                     const DecodeParams& p, int n_items, int num_sms, cudaStream_t stream) {
+  switch (group) {
+    case 1: return launch_t<D, 1, E>(km, vm, p, n_items, num_sms, stream);
+    case 2: return launch_t<D, 2, E>(km, vm, p, n_items, num_sms, stream);
+    case 4: return launch_t<D, 4, E>(km, vm, p, n_items, num_sms, stream);
+    case 8: return launch_t<D, 8, E>(km, vm, p, n_items, num_sms, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+template <class E>
+cudaError_t launch_d(int head_dim, int group, const CUtensorMap& km, const CUtensorMap& vm,
+                     const DecodeParams& p, int n_items, int num_sms, cudaStream_t stream) {
+  switch (head_dim) {
+    case 64: return launch_g<64, E>(group, km, vm, p, n_items, num_sms, stream);
+    case 128: return launch_g<128, E>(group, km, vm, p, n_items, num_sms, stream);
+    case 256: return launch_g<256, E>(group, km, vm, p, n_items, num_sms, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_decode_page8(int head_dim, int group, int dtype, const CUtensorMap& km,
+                                const CUtensorMap& vm, const DecodeParams& p, int n_items,
+                                int num_sms, cudaStream_t stream) {
+  if (n_items <= 0 || num_sms <= 0) return cudaSuccess;
+  switch (dtype) {
+    case FI_DTYPE_BF16: return launch_d<Bf16>(head_dim, group, km, vm, p, n_items, num_sms, stream);
+    case FI_DTYPE_FP16: return launch_d<Fp16>(head_dim, group, km, vm, p, n_items, num_sms, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace fi

@@ -67,6 +67,10 @@ constexpr int32_t kStepMaxRequests = 262144;
 constexpr int32_t kStepMaxPageSize = 1024;
 
 inline int decode_tile_tokens(int head_dim) { return 8192 / head_dim; }  // 32 KB of K+V
+// The kernels over a page-scaled FP8 cache: tokens per tile of the decode
+// kernel; M rows (query rows x the g heads of a kv head) of a prefill item.
+constexpr int kPage8DecodeTile = 128;
+inline int page8_prefill_rows(int head_dim) { return head_dim <= 128 ? 256 : 128; }
 // A batch with both decode rows and multi-row (chunked prefill) requests runs
 // as one persistent launch of the mixed kernel for these shapes (q/out and
 // cache of one 16-bit type, head_dim 256, 1, 2 or 4 query heads per kv head).

@@ -131,6 +131,14 @@ cudaError_t launch_mixed(int head_dim, int group, int dtype, const CUtensorMap& 
 cudaError_t launch_decode(int head_dim, int group, int dtype, int kv_dtype, const CUtensorMap& km,
                           const CUtensorMap& vm, const DecodeParams& p, int n_items, int num_sms,
                           cudaStream_t stream);
+// Over a page-scaled FP8 cache (decode_page8.cu, prefill_page8.cu); the
+// params' k_head_scale / v_head_scale are then [num_pages][num_kv_heads].
+cudaError_t launch_decode_page8(int head_dim, int group, int dtype, const CUtensorMap& km,
+                                const CUtensorMap& vm, const DecodeParams& p, int n_items,
+                                int num_sms, cudaStream_t stream);
+cudaError_t launch_prefill_page8(int head_dim, int dtype, const CUtensorMap& qm,
+                                 const CUtensorMap& km, const CUtensorMap& vm,
+                                 const PrefillParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_merge(const MergeParams& p, int n_rows, cudaStream_t stream);
 
 // fi_page_table_step (page_step.cu): the arguments of the call, and the step

@@ -34,7 +34,9 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
   if (opt.window_left < -1) return FI_ERR_INVALID_ARG;
   if (opt.dtype != FI_DTYPE_BF16 && opt.dtype != FI_DTYPE_FP16) return FI_ERR_INVALID_ARG;
   const int32_t kv_dtype = opt.kv_dtype < 0 ? opt.dtype : opt.kv_dtype;
-  if (kv_dtype != opt.dtype && kv_dtype != FI_DTYPE_E4M3) return FI_ERR_INVALID_ARG;
+  if (kv_dtype != opt.dtype && kv_dtype != FI_DTYPE_E4M3 && kv_dtype != FI_DTYPE_E4M3_PAGE)
+    return FI_ERR_INVALID_ARG;
+  const bool page8 = kv_dtype == FI_DTYPE_E4M3_PAGE;
   if (mode != FI_MODE_DECODE && mode != FI_MODE_PREFILL) return FI_ERR_INVALID_ARG;
   if (batch < 0 || num_sms <= 0) return FI_ERR_INVALID_ARG;
   if (num_qo_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || page_size <= 0)
@@ -60,8 +62,8 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
   p.window_left = opt.window_left;
   p.dtype = opt.dtype;
   p.kv_dtype = kv_dtype;
-  // an FP8 cache is read by the decode kernel only
-  if (kv_dtype == FI_DTYPE_E4M3 && mode != FI_MODE_DECODE) return FI_ERR_UNSUPPORTED;
+  // an FP8 cache without page scales is read by the decode kernel only
+  if ((kv_dtype == FI_DTYPE_E4M3 || page8) && mode != FI_MODE_DECODE) return FI_ERR_UNSUPPORTED;
 
   // ---- validate the page table and the query packing; kv_len per request
   std::vector<int64_t> kv_len(batch), qo_len(batch), qo_start(batch);
@@ -108,7 +110,7 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
   if (G < 0) return FI_ERR_INVALID_ARG;
   if (G > 0) {
     if (!opt.prefix_group_indptr || !opt.prefix_pages) return FI_ERR_INVALID_ARG;
-    if (mode != FI_MODE_DECODE || kv_dtype == FI_DTYPE_E4M3 || opt.window_left >= 0)
+    if (mode != FI_MODE_DECODE || kv_dtype == FI_DTYPE_E4M3 || page8 || opt.window_left >= 0)
       return FI_ERR_UNSUPPORTED;
     const int32_t* gi = opt.prefix_group_indptr;
     if (gi[0] < 0 || gi[G] > batch) return FI_ERR_INVALID_ARG;
@@ -160,7 +162,7 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
 
   // ---- decode work: every request with exactly one query row. Chunks start
   //      on page boundaries from the page holding the first visible key.
-  const int tile = decode_tile_tokens(head_dim);
+  const int tile = page8 ? kPage8DecodeTile : decode_tile_tokens(head_dim);
   std::vector<int> dec;
   int64_t dec_tiles = 0;
   for (int b = 0; b < batch; ++b) {
@@ -295,15 +297,19 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
   // ---- prefill work: requests with two or more query rows, one item per
   //      (query tile of kPrefillTileM rows, query head); the tiles are
   //      ordered longest first, the heads of a tile stay together, in head
-  //      order (the two-tile kernel runs items 2p and 2p + 1 in one CTA)
+  //      order (the two-tile kernel runs items 2p and 2p + 1 in one CTA).
+  //      Over a page-scaled cache an item is a kv head with all its query
+  //      heads: tile_rows rows x g heads fill the kernel's M rows.
+  const int64_t tile_rows = page8 ? page8_prefill_rows(head_dim) / g : kPrefillTileM;
+  const int64_t heads_per_tile = page8 ? num_kv_heads : num_qo_heads;
   struct Tile { int64_t len, kv_begin, kv_end; int32_t b, qt; };
   std::vector<Tile> tiles;
   for (int b = 0; b < batch; ++b) {
     if (qo_len[b] < 2) continue;
-    const int64_t n_qt = ceil_div(qo_len[b], kPrefillTileM);
+    const int64_t n_qt = ceil_div(qo_len[b], tile_rows);
     for (int64_t qt = 0; qt < n_qt; ++qt) {
-      const int64_t r0 = qt * kPrefillTileM;
-      const int64_t r_last = std::min<int64_t>(qo_len[b], r0 + kPrefillTileM) - 1;
+      const int64_t r0 = qt * tile_rows;
+      const int64_t r_last = std::min<int64_t>(qo_len[b], r0 + tile_rows) - 1;
       int64_t kv_end = kv_len[b];
       if (p.causal) kv_end = std::min<int64_t>(kv_len[b], kv_len[b] - qo_len[b] + r_last + 1);
       // the tile's first row has the smallest window start; tiles of keys
@@ -337,8 +343,8 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
   pieces.reserve(tiles.size());
   {
     const int64_t kv_tile = prefill_kv_tile(head_dim);
-    const int64_t heads_per_unit = (head_dim <= 128 && g % 2 == 0) ? 2 : 1;
-    const int64_t units = int64_t(tiles.size()) * (num_qo_heads / heads_per_unit);
+    const int64_t heads_per_unit = (!page8 && head_dim <= 128 && g % 2 == 0) ? 2 : 1;
+    const int64_t units = int64_t(tiles.size()) * (heads_per_tile / heads_per_unit);
     int64_t split_len = 0;   // keys per piece (whole KV tiles); 0: no split
     if (dec.empty() && !tiles.empty() && units < 2 * int64_t(num_sms)) {
       const int64_t max_tiles = ceil_div(tiles[0].len, kv_tile);
@@ -363,11 +369,11 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
         continue;
       }
       // slots of the tile's rows: row r, piece j -> slot s0 + r * k + j
-      const int64_t rows = std::min<int64_t>(kPrefillTileM, qo_len[t.b] - int64_t(t.qt) * kPrefillTileM);
+      const int64_t rows = std::min<int64_t>(tile_rows, qo_len[t.b] - int64_t(t.qt) * tile_rows);
       const int64_t s0 = p.num_slots;
       p.num_slots += int32_t(rows * k);
       for (int64_t r = 0; r < rows; ++r) {
-        MergeTask mt{int32_t(qo_start[t.b] + int64_t(t.qt) * kPrefillTileM + r),
+        MergeTask mt{int32_t(qo_start[t.b] + int64_t(t.qt) * tile_rows + r),
                      int32_t(s0 + r * k), int32_t(k), -1, 0, 0, {0, 0}};
         p.prefill_merges.push_back(mt);
       }
@@ -380,7 +386,7 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
     std::stable_sort(pieces.begin(), pieces.end(),
                      [](const Piece& x, const Piece& y) { return x.len > y.len; });
   }
-  p.prefill_items.resize(pieces.size() * size_t(num_qo_heads));
+  p.prefill_items.resize(pieces.size() * size_t(heads_per_tile));
   WorkItem* pdst = p.prefill_items.data();
   for (const Piece& t : pieces) {
     WorkItem w;
@@ -390,9 +396,9 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
     w.tok_begin = int32_t(t.kv_begin);
     w.tok_end = int32_t(t.kv_end);
     w.slot = t.slot;   // a piece: its state of row r at slot + r * merge
-    w.q_row = int32_t(qo_start[t.b] + int64_t(t.qt) * kPrefillTileM);
+    w.q_row = int32_t(qo_start[t.b] + int64_t(t.qt) * tile_rows);
     w.merge = t.k;     // a piece: the tile's piece count; else -1
-    for (int h = 0; h < num_qo_heads; ++h) {
+    for (int h = 0; h < heads_per_tile; ++h) {
       w.head = h;
       *pdst++ = w;
     }

@@ -331,6 +331,52 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t smem_addr, uint32_t lbo
   return d;
 }
 
+// The same descriptor for any swizzle: `mode` is 0 (none), 2 (128-byte), 4
+// (64-byte) or 6 (32-byte). 64-byte swizzle: rows of 64 B, 8-row atoms of
+// 512 B; MN-major without swizzle: 16 B along MN per row of K, 8 rows
+// adjacent, `lbo` between 8-row groups along K and `sbo` between 16-byte
+// groups along MN.
+__device__ __forceinline__ uint64_t sdesc_swz(uint32_t smem_addr, uint32_t lbo, uint32_t sbo,
+                                              uint32_t mode) {
+  uint64_t d = 0;
+  d |= uint64_t((smem_addr >> 4) & 0x3FFFu);
+  d |= uint64_t((lbo >> 4) & 0x3FFFu) << 16;
+  d |= uint64_t((sbo >> 4) & 0x3FFFu) << 32;
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(mode) << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[smem] * B[smem], kind::f8f6f4 (here e4m3 inputs, 32 elements
+// of K per instruction, fp32 accumulate).
+__device__ __forceinline__ void tc_mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor, kind::f8f6f4 with e4m3 A and B, fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) |
+         (uint32_t(M >> 4) << 24);
+}
+
+// Four bytes from global to shared memory, completing asynchronously; the
+// calling thread's copies so far arrive on an mbarrier when they have landed.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // Instruction descriptor, kind::f16: A and B of one 16-bit type (`fmt`: 0 =
 // fp16, 1 = bf16), fp32 accumulator, M x N. a_mn / b_mn select MN-major
 // (transposed) operands.

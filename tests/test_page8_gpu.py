@@ -1,0 +1,213 @@
+"""Attention over a page-scaled FP8 cache on the GPU against a plain float64
+implementation (the bounds are derived in _page8.py)."""
+import numpy as np
+import pytest
+
+from paged_kv_attention_27_gb300 import binding as B
+
+from . import _page8
+from ._gpu import ensure_built
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ensure_built()
+    return B.lib()
+
+
+def _check(b, sms=None, what="", **kw):
+    d = _page8.Device(b, sms)
+    out, lse = d.run(**kw)
+    assert d.status() == B.FI_OK
+    _page8.compare(b, out, lse, _page8.reference(b, **kw), what=what)
+    return d
+
+
+LENS = [0, 1, 15, 16, 17, 127, 128, 129, 300, 700, 0, 45]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("g", [1, 2, 4, 8])
+@pytest.mark.parametrize("layout,P,dtype", [("NHD", 16, "bf16"), ("HND", 32, "bf16"),
+                                            ("HND", 16, "fp16"), ("NHD", 32, "fp16")])
+def test_decode_shapes(d, g, layout, P, dtype):
+    b = _page8.Batch(LENS, 2 * g, 2, d, P, layout, dtype, seed=d + g, tail=0x7f)
+    _check(b, what=f"d{d} g{g} {layout} {dtype}")
+
+
+@pytest.mark.parametrize("sms", [1, 3, 152, 2000])
+@pytest.mark.parametrize("g,d", [(8, 128), (1, 64), (4, 256)])
+def test_decode_splits(sms, g, d):
+    b = _page8.Batch([5000, 1, 1300, 2049, 0, 640], 2 * g, 2, d, 16, seed=7)
+    _check(b, sms, what=f"sms {sms}")
+
+
+@pytest.mark.parametrize("w", [0, 1, 15, 16, 17, 127, 128, 300, 5000])
+@pytest.mark.parametrize("g,d", [(8, 128), (2, 64), (1, 256)])
+def test_decode_window(w, g, d):
+    b = _page8.Batch([1, 16, 40, 333, 1500], 2 * g, 2, d, 16, window=w, seed=w, tail=0xff)
+    # keys before the window, on its first page too, hold NaN codes
+    for r, n in enumerate(b.kv_lens):
+        for t in range(max(0, n - 1 - w)):
+            page = b.page_indices[b.page_indptr[r] + t // 16]
+            for c in b.codes:
+                c[page, t % 16] = 0x7f
+    ref_b = _page8.Batch([1, 16, 40, 333, 1500], 2 * g, 2, d, 16, window=w, seed=w)
+    dv = _page8.Device(b)
+    out, lse = dv.run()
+    assert dv.status() == B.FI_OK
+    _page8.compare(b, out, lse, _page8.reference(ref_b), what=f"window {w}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("g,d", [(8, 128), (1, 128), (4, 64), (2, 256)])
+def test_decode_any_scales(g, d, dtype):
+    """Scales that are no powers of two, and pages whose values (and so their
+    scales) differ by 2^24; tensor-wide scales on top."""
+    b = _page8.Batch([900, 33, 257], 2 * g, 2, d, 16, dtype=dtype, seed=3, scales="any")
+    _check(b, what="any", k_scale=0.5, v_scale=3.0)
+    b = _page8.Batch([900, 33, 257], 2 * g, 2, d, 16, seed=4, v_spread=12)
+    _check(b, what="spread")
+
+
+def test_decode_small_scale_pages_keep_their_weight():
+    """The page with all the weight has values 2^40 times smaller than the
+    others': its own values have to come out."""
+    import torch
+    b = _page8.Batch([64], 8, 1, 128, 16, seed=5)
+    b.codes[0][:] = 0x38                      # every key element 1
+    for s in b.scale:
+        s[:] = 1.0
+    b.scale[0][b.page_indices[2], 0] = 64.0   # keys of page 2: 64
+    b.scale[1][b.page_indices[2], 0] = 2.0 ** -40
+    b.q = torch.ones_like(b.q)
+    _check(b, what="small page")
+
+
+def test_decode_q_range_and_special_values():
+    """q elements over fp16's and bf16's whole range of a row, a zero row, and
+    rows with a NaN or an infinity, which stay their own."""
+    import torch
+    for dtype, lo in (("bf16", -30), ("fp16", -12)):
+        b = _page8.Batch([200] * 6, 4, 1, 128, 16, dtype=dtype, seed=6)
+        e = torch.from_numpy(np.random.default_rng(1).integers(lo, 1, (6, 4, 128)))
+        b.q = (b.q.double() * torch.exp2(e.double())).to(b.q.dtype)
+        b.q[1] = 0
+        _check(b, what=f"range {dtype}")
+        b.q[2, 1, 5] = float("nan")
+        b.q[3, 2, 7] = float("inf")
+        d = _page8.Device(b)
+        out, lse = d.run()
+        bad = torch.isnan(out).all(dim=2).cpu().numpy()
+        want = np.zeros((6, 4), dtype=bool)
+        want[2, 1] = want[3, 2] = True
+        assert np.array_equal(bad, want) and np.array_equal(torch.isnan(lse).cpu().numpy(), want)
+        assert np.array_equal(torch.isnan(out).any(dim=2).cpu().numpy(), want)
+
+
+def test_decode_sm_scale_zero_is_the_mean():
+    b = _page8.Batch([70, 16, 129], 8, 2, 64, 16, seed=8)
+    b.sm_scale = 0.0
+    _check(b, what="mean")
+
+
+def test_decode_deterministic_and_without_lse():
+    import torch
+    b = _page8.Batch([3000, 50, 900, 2000], 16, 2, 128, 16, seed=9)
+    d = _page8.Device(b, 40)
+    o1, l1 = [x.clone() for x in d.run()]
+    for _ in range(3):
+        d.out.fill_(7)
+        o2, l2 = d.run()
+        assert torch.equal(o1, o2) and torch.equal(l1, l2)
+    d.lse.fill_(-3)
+    d.run(lse=False)
+    assert torch.equal(d.out, o1) and bool((d.lse == -3).all())
+
+
+def test_decode_page_views_of_one_buffer():
+    import torch
+    b = _page8.Batch([100, 40], 8, 2, 128, 16, seed=10)
+    d = _page8.Device(b)
+    o1 = d.run()[0].clone()
+    kv = torch.zeros(b.num_pages, 2, 16, 2, 128, dtype=torch.uint8, device="cuda")
+    kv[:, 0], kv[:, 1] = d.k, d.v
+    d.k, d.v = kv, kv[:, 1]
+    d.out.zero_()
+    assert torch.equal(d.run(page_stride=2 * 16 * 2 * 128)[0], o1)
+
+
+def test_decode_page_outside_the_cache_is_skipped_and_reported():
+    b = _page8.Batch([100, 60], 8, 2, 128, 16, seed=11)
+    d = _page8.Device(b)
+    want = _page8.reference(b)
+    d.page_indices[2] = b.num_pages
+    d.page_indices[3] = -1
+    out, lse = d.run()
+    assert d.status() == B.FI_ERR_DEVICE_BOUNDS
+    rows = np.array([1])
+    _page8.compare(b, out, lse, want, rows=rows, what="other request")
+    # the request itself: its keys without the two pages
+    q, k, v = b.q64()[0], b.kv64(0), b.kv64(1)
+    t = np.array([x for x in range(100) if x // 16 not in (2, 3)])
+    pages = b.page_indices[t // 16]
+    for h in range(8):
+        s = b.sm_scale * (k[pages, t % 16, h // 4] @ q[h])
+        p = np.exp(s - s.max())
+        o = p @ v[pages, t % 16, h // 4] / p.sum()
+        assert np.abs(out[0, h].double().cpu().numpy() - o).max() < 2e-2
+        assert abs(lse[0, h].item() - (s.max() + np.log(p.sum()))) < 1e-4
+    d.page_indices[2], d.page_indices[3] = int(b.page_indices[2]), int(b.page_indices[3])
+    _page8.compare(b, *d.run(), want, what="after")
+    assert d.status() == B.FI_OK
+
+
+@pytest.mark.parametrize("d,g", [(128, 8), (64, 1), (256, 4)])
+def test_decode_bounded_wait_and_recovery(d, g):
+    b = _page8.Batch([300, 40, 1000], 2 * g, 2, d, 16, seed=12)
+    dv = _page8.Device(b)
+    B.fi_debug_set_fault(1, 50_000_000)
+    try:
+        dv.run()
+        assert dv.status() == B.FI_ERR_DEVICE_TIMEOUT
+    finally:
+        B.fi_debug_set_fault(0, 0)
+    _page8.compare(b, *dv.run(), _page8.reference(b), what="after")
+    assert dv.status() == B.FI_OK
+
+
+def test_decode_through_host_buffers_and_without_workspace():
+    import torch
+    b = _page8.Batch([500, 3, 0, 64], 8, 2, 128, 16, seed=13)
+    d = _page8.Device(b)
+    o1, l1 = [x.clone() for x in d.run()]
+    d.out.zero_()
+    B.fi_batch_decode_paged_noalloc(d.plan, d.q, d.k, d.v, B.FI_LAYOUT_NHD, 0, b.num_pages,
+                                    d.page_indptr, d.page_indices, d.last_page_len, b.sm_scale, 1.0,
+                                    1.0, d.out, d.lse, k_head_scale=d.ks, v_head_scale=d.vs)
+    torch.cuda.synchronize()
+    assert torch.equal(d.out, o1) and torch.equal(d.lse, l1)
+    info = B.fi_plan_get_info(d.plan)
+    ws = torch.empty(info["workspace_bytes"] + info["host_io_bytes"], dtype=torch.uint8, device="cuda")
+    oh, lh = torch.empty(o1.shape, dtype=o1.dtype), torch.empty(l1.shape)
+    B.fi_batch_attention_host(d.plan, b.q.contiguous(), None, d.k, d.v, B.FI_LAYOUT_NHD, 0,
+                              b.num_pages, b.page_indptr, b.page_indices, b.last_page_len,
+                              b.sm_scale, 1.0, 1.0, oh, lh, ws, ws.numel(), k_head_scale=d.ks,
+                              v_head_scale=d.vs)
+    assert torch.equal(oh, o1.cpu()) and torch.equal(lh, l1.cpu())
+
+
+def test_decode_on_another_stream():
+    import torch
+    b = _page8.Batch([2000, 64, 333], 8, 2, 128, 16, seed=14)
+    d = _page8.Device(b)
+    o1 = d.run()[0].clone()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        d.out.zero_()
+        d.run()
+    s.synchronize()
+    assert torch.equal(d.out, o1)
