@@ -86,7 +86,7 @@ typedef enum { FI_MODE_DECODE = 0, FI_MODE_PREFILL = 1 } fi_mode;
 /* Element types: q and out are bf16 or fp16; the K/V cache is the same type
  * or FP8 E4M3 (OCP format): FI_DTYPE_E4M3 with a scale per tensor and kv head
  * (decode plans only), FI_DTYPE_E4M3_PAGE with a scale for each (page, kv
- * head) of K and of V (decode plans only). lse and partial states are
+ * head) of K and of V (decode and prefill plans). lse and partial states are
  * fp32. */
 typedef enum {
   FI_DTYPE_BF16 = 0,
@@ -110,8 +110,8 @@ typedef enum {
  *                an FP8 cache (decode plans only; FI_ERR_UNSUPPORTED for
  *                prefill plans). An FP8 cache holds K / k_scale and
  *                V / v_scale; the run calls take the two scales. Or
- *                FI_DTYPE_E4M3_PAGE for an FP8 cache with page scales (decode plans
- *                only): page p of kv head h holds K / s and V / s' with its
+ *                FI_DTYPE_E4M3_PAGE for an FP8 cache with page scales (either
+ *                mode): page p of kv head h holds K / s and V / s' with its
  *                own s = k_head_scale[p * num_kv_heads + h] and s' from
  *                v_head_scale; fi_append_paged_kv fills such a cache.
  *   num_prefix_groups, prefix_group_indptr, prefix_pages

@@ -23,7 +23,7 @@ LIB = os.path.join(LIBDIR, "libfi.so")
 
 SOURCES = ["plan.cpp", "api.cu", "decode.cu", "merge.cu", "prefill.cu", "prefill_pair.cu",
            "noalloc.cu", "page_step.cu", "append.cu",
-           "decode_page8.cu"]
+           "decode_page8.cu", "prefill_page8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

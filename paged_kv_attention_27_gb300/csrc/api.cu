@@ -585,7 +585,9 @@ fi_status run_paged(fi_plan_t plan, bool prefill_call, const void* q, const int3
       dstream = side.stream;
     }
     if (!P.prefill_items.empty()) {
-      e = fi::launch_prefill(P.head_dim, P.dtype, qmap, kmap, vmap, pp, P.num_sms, stream);
+      e = page8 ? fi::launch_prefill_page8(P.head_dim, P.dtype, qmap, kmap, vmap, pp, P.num_sms,
+                                           stream)
+                : fi::launch_prefill(P.head_dim, P.dtype, qmap, kmap, vmap, pp, P.num_sms, stream);
       if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
     }
     if (!P.prefill_merges.empty()) {

@@ -63,7 +63,7 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
   p.dtype = opt.dtype;
   p.kv_dtype = kv_dtype;
   // an FP8 cache without page scales is read by the decode kernel only
-  if ((kv_dtype == FI_DTYPE_E4M3 || page8) && mode != FI_MODE_DECODE) return FI_ERR_UNSUPPORTED;
+  if (kv_dtype == FI_DTYPE_E4M3 && mode != FI_MODE_DECODE) return FI_ERR_UNSUPPORTED;
 
   // ---- validate the page table and the query packing; kv_len per request
   std::vector<int64_t> kv_len(batch), qo_len(batch), qo_start(batch);

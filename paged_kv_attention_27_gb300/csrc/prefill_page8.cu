@@ -1,0 +1,828 @@
+// Variable-length batch prefill over a page-scaled FP8 cache: chunks of query
+// rows, causal or not, against K = s_k(page, head) * codes, V alike.
+//
+// A work item is (rows of a request, kv head): rows x the g query heads of the
+// kv head fill the M rows of two 128-row tiles (one at head_dim 256), heads
+// inner, so that every K/V tile that is loaded serves all of them; a draft's
+// few rows and a long prompt run the same way.
+//
+// Arithmetic: codes are exact in fp16, so both products run as fp16 tcgen05
+// MMAs (fp32 accumulators in TMEM) on tiles that a warpgroup widens from the
+// cache bytes. A bf16 q row is widened too: times the power of two that puts
+// its largest element at 2^13..2^14, exact down to 2^-37 of that element; fp16
+// q enters as it is. The page's s_k joins the row's score scale, one factor per
+// 16 columns. The page's s_v joins the weight before it is rounded to fp16:
+//   w = 2^(s + log2 s_v - m),  m the running maximum of s + log2 s_v,
+//   O = sum w code,  l = sum w r / s_v (r: s_v of the item's first page),
+//   out = O r / l,   lse = ln 2 (m + log2 l - log2 r):
+// one exponential per score, and both sums keep their leading bits whatever
+// the spread of the scales.
+//
+// Roles (TILES = 2: 16 warps; TILES = 1: 12): a softmax warpgroup per tile
+// (thread = M row = TMEM lane; they take turns so that one tile's MMAs run
+// under the other's softmax), then the epilogue; a warp each to issue a tile's
+// MMAs, to copy K/V pages and their scales, to copy Q; a warpgroup to widen.
+// Bound: tensor cores and the exponentials (16 per cycle), which at head_dim
+// 128 take the same time; widening costs 2 / 256 of the MMA work's
+// instructions' worth per row and runs beside both.
+#include <cfloat>
+#include <climits>
+#include <type_traits>
+
+#include "elem.cuh"
+#include "fi_internal.h"
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace fi {
+
+namespace {
+
+using namespace dev;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// log2 units: the maximum moves when a score passes it by more; weights stay
+// at or below 2^8, inside fp16
+constexpr float kRescaleThreshold = 8.0f;
+constexpr int kItemRing = 8;
+// tiles whose page scales are kept: K of tile t is widened once S of tile t - 2
+// is complete, which was issued after the softmax of tile t - 3
+constexpr int kScaleRing = 4;
+
+template <int D>
+struct P8Cfg {
+  static constexpr int TILES = D <= 128 ? 2 : 1;
+  static constexpr int M = 128;
+  static constexpr int N = D <= 128 ? 128 : 64;             // keys per tile
+  static constexpr int NG = N / 16;                         // 16-column groups (pages) of a tile
+  static constexpr int DBLK = D / 64;                       // 128-byte slices of an fp16 row
+  static constexpr int RAW_ROW = D < 128 ? D : 128;         // bytes of a row of codes
+  static constexpr int RAW_BLK = D <= 128 ? 1 : D / 128;
+  static constexpr int RAW = N * D;                         // one K (or V) tile of codes
+  static constexpr int NRAW = D == 64 ? 2 : 1;              // code tiles of K (and of V) in flight
+  static constexpr int KV = N * D * 2;                      // one widened tile
+  static constexpr int Q = M * D * 2;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + TILES * Q;           // two
+  static constexpr int OFF_V = OFF_K + 2 * KV;              // two
+  static constexpr int OFF_RAW = OFF_V + 2 * KV;            // K tiles, then V tiles
+  static constexpr int USED = OFF_RAW + 2 * NRAW * RAW;
+  static constexpr int SMEM = (USED < 120 * 1024 ? 120 * 1024 : USED) + 1024;   // one CTA per SM
+  static constexpr int SOFT = 4 * TILES;                    // softmax warps
+  static constexpr int W_MMA = SOFT, W_KV = SOFT + 2, W_Q = SOFT + 3, W_WIDE = SOFT + 4;
+  static constexpr int THREADS = 32 * (SOFT + 8);
+  // registers per thread at launch and, per warpgroup, after the split
+  static constexpr uint32_t LAUNCH_REGS = TILES == 2 ? 128 : 168;
+  static constexpr uint32_t SOFT_REGS = TILES == 2 ? 192 : 240;
+  static constexpr uint32_t HELP_REGS = TILES == 2 ? 56 : 104;
+  static constexpr uint32_t WIDE_REGS = TILES == 2 ? 72 : 160;
+  static_assert(TILES * SOFT_REGS + HELP_REGS + WIDE_REGS <= (TILES + 2) * LAUNCH_REGS, "");
+  static constexpr uint32_t TMEM_COLS = 512;
+  __host__ __device__ static constexpr uint32_t col_s(int i) { return uint32_t(i * N); }
+  __host__ __device__ static constexpr uint32_t col_o(int i) { return uint32_t(TILES * N + i * D); }
+  static_assert(TILES * (N + D) <= 512, "TMEM budget");
+  static constexpr uint32_t IDESC_QK = idesc_f16kind(M, N, 0, 0, Fp16::kMmaFmt);
+  static constexpr uint32_t IDESC_PV = idesc_f16kind(M, D, 0, 1, Fp16::kMmaFmt);
+};
+
+struct P8Barriers {
+  uint64_t item_full[kItemRing], item_empty[kItemRing];
+  uint64_t q_raw, q_full, q_empty;
+  uint64_t kr_full[2], kr_empty[2], vr_full[2], vr_empty[2];   // code tiles
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];       // widened tiles
+  uint64_t s_full[2], p_full[2], pv_done[2], o_final[2], drain[2];
+  uint64_t sc_full[kScaleRing];                                // a tile's page scales
+  uint64_t turn[2];                                            // the softmax warpgroups' turns
+};
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+template <int D, class E>
+__global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
+prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
+                     const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map, PrefillParams prm) {
+  using C = P8Cfg<D>;
+  constexpr bool kWidenQ = std::is_same<E, Bf16>::value;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) P8Barriers bars;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_flag;
+  __shared__ int item_ring[kItemRing];
+  __shared__ __align__(8) float2 raw_scale[2][8];           // per page of a code tile: s_k, s_v
+  __shared__ __align__(16) float4 scale_sh[kScaleRing][8];  // per 16 columns: s_k (-1: no page),
+                                                            // log2 s_v, r / s_v, r
+  __shared__ int lost_sh[kScaleRing];                       // the tile has a page outside the cache
+  __shared__ uint8_t q_exp[2][C::TILES * 128];              // q rows' exponents + 128, by item parity
+
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t limit = prm.wait_limit_ns;
+  const int P = prm.page_size, ppt = C::N / P;
+  const int g = prm.group;
+  const int R = C::M / g;                                   // query rows per tile
+  const int hkv = prm.num_qo_heads / g;
+
+  auto item_at = [&](int n, int& idx) {
+    if (!mbar_wait_bounded(smem_u32(&bars.item_full[n % kItemRing]), (n / kItemRing) & 1, limit,
+                           &abort_flag))
+      return false;
+    idx = *reinterpret_cast<volatile int*>(&item_ring[n % kItemRing]);
+    return true;
+  };
+  auto item_done = [&](int n) { mbar_arrive(smem_u32(&bars.item_empty[n % kItemRing])); };
+  // item n for a whole warp (lane 0 waits)
+  auto take_item = [&](int n, int& idx) {
+    int v = -1;
+    bool good = true;
+    if (lane == 0) {
+      good = item_at(n, v);
+      item_done(n);
+    }
+    idx = __shfl_sync(0xffffffffu, v, 0);
+    return __shfl_sync(0xffffffffu, good, 0) != 0;
+  };
+  auto tiles_of = [&](const WorkItem& w) { return (w.tok_end - w.tok_begin + C::N - 1) / C::N; };
+  // whether tile i of the item has a row (tile 0 always does)
+  auto active = [&](const WorkItem& w, int i) {
+    return i == 0 || w.q_row + R < prm.qo_indptr[w.req + 1];
+  };
+  auto fail = [&] {
+    abort_flag = 1;
+    atomicOr(prm.err, kErrTimeout);
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kItemRing; ++s) {
+      mbar_init(smem_u32(&bars.item_full[s]), 1);
+      // softmax warps, MMA warps, the Q warp, the widening warps
+      mbar_init(smem_u32(&bars.item_empty[s]), C::SOFT + C::TILES + 1 + 4);
+    }
+    mbar_init(smem_u32(&bars.q_raw), 1);
+    mbar_init(smem_u32(&bars.q_full), 4);
+    mbar_init(smem_u32(&bars.q_empty), C::TILES);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&bars.kr_full[s]), 1 + ppt);       // the bytes, and each page's scales
+      mbar_init(smem_u32(&bars.kr_empty[s]), 4);
+      mbar_init(smem_u32(&bars.vr_full[s]), 1);
+      mbar_init(smem_u32(&bars.vr_empty[s]), 4);
+      mbar_init(smem_u32(&bars.k_full[s]), 4);
+      mbar_init(smem_u32(&bars.k_empty[s]), C::TILES);
+      mbar_init(smem_u32(&bars.v_full[s]), 4);
+      mbar_init(smem_u32(&bars.v_empty[s]), C::TILES);
+      mbar_init(smem_u32(&bars.s_full[s]), 1);
+      mbar_init(smem_u32(&bars.p_full[s]), 4);
+      mbar_init(smem_u32(&bars.pv_done[s]), 1);
+      mbar_init(smem_u32(&bars.o_final[s]), 1);
+      mbar_init(smem_u32(&bars.drain[s]), 1);
+      mbar_init(smem_u32(&bars.turn[s]), 4);
+    }
+    for (int s = 0; s < kScaleRing; ++s) mbar_init(smem_u32(&bars.sc_full[s]), 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == C::W_MMA) {
+    tmem_alloc(smem_u32(&tmem_base_sh), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  int issued = 0;    // the K/V copy warp: tiles whose copies it has issued
+  int q_loads = 0;   // the Q copy warp
+
+  if (warp >= C::W_WIDE) {
+    // ------------------------------------------------------------------ widening
+    if constexpr (C::WIDE_REGS < C::LAUNCH_REGS) setmaxnreg_dec<C::WIDE_REGS>();
+    const int ct = threadIdx.x - C::W_WIDE * 32;            // 0..127
+    // Codes -> fp16 rows as the TMA would write them (128-byte swizzled slices
+    // of 64 dimensions). A warp's lanes take 8 rows x 4 chunks of 16 codes:
+    // reads and writes then touch all banks evenly. Rows from `valid` on, and
+    // those of pages outside the cache (bits of `lost`), become zero.
+    auto widen = [&](uint32_t src, uint32_t dst, int valid, uint32_t lost) {
+      constexpr int CH = D / 16;                            // 16-code chunks per row
+      constexpr int ITER = C::N * CH / 128;
+#pragma unroll 4
+      for (int i = 0; i < ITER; ++i) {
+        const int unit = i * 16 + (ct >> 3);                // 8-row block x chunk
+        const int row = (unit / CH) * 8 + (ct & 7), ch = unit % CH;
+        uint32_t at;
+        if constexpr (D == 64) at = row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
+        else at = (ch >> 3) * C::N * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+        const uint4 u = lds128(src + at);
+        uint4 lo, hi;
+        lo.x = E4m3::to_f16x2(u.x); lo.y = E4m3::to_f16x2(u.x >> 16);
+        lo.z = E4m3::to_f16x2(u.y); lo.w = E4m3::to_f16x2(u.y >> 16);
+        hi.x = E4m3::to_f16x2(u.z); hi.y = E4m3::to_f16x2(u.z >> 16);
+        hi.z = E4m3::to_f16x2(u.w); hi.w = E4m3::to_f16x2(u.w >> 16);
+        if (row >= valid || ((lost >> (row >> 4)) & 1u)) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t to = dst + (ch >> 2) * C::N * 128 + row * 128;
+        const int c = (ch & 3) * 2, x = row & 7;
+        st_shared_v4(to + ((c ^ x) << 4), lo);
+        st_shared_v4(to + (((c + 1) ^ x) << 4), hi);
+      }
+    };
+    bool ok = true;
+    int gt = 0;   // tiles of earlier items
+    for (int n = 0; ok; ++n) {
+      int it = -1;
+      ok = take_item(n, it);
+      if (!ok || it < 0) break;
+      const WorkItem w = prm.items[it];
+      const int nt = tiles_of(w);
+      float ref = 1.f;
+      // q rows to fp16 in place (each thread a row of each tile)
+      auto widen_q = [&] {
+        if (!mbar_wait_warp(smem_u32(&bars.q_raw), n & 1, limit, &abort_flag)) return false;
+        if constexpr (kWidenQ) {
+#pragma unroll 1
+          for (int i = 0; i < C::TILES; ++i) {
+            // (any order of a row's 16-byte pieces does; this one spreads the
+            // lanes over the banks)
+            const uint32_t row = base + C::OFF_Q + i * C::Q + ct * 128;
+            auto piece = [&](int c) {
+              return row + (c >> 3) * C::M * 128 + (((c ^ ct) & 7) << 4);
+            };
+            float a = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < D / 8; ++c) {
+              float f[8];
+              unpack8<E>(lds128(piece(c)), f);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float b = fabsf(f[e]);
+                a = b < INFINITY ? fmaxf(a, b) : a;
+              }
+            }
+            // q' = q 2^(13 - e) with 2^e <= a < 2^(e + 1)
+            const int e2 = max(int(__float_as_uint(a) >> 23) - 127, -100);
+            const float up = __uint_as_float(uint32_t(127 + min(13 - e2, 127)) << 23);
+#pragma unroll 4
+            for (int c = 0; c < D / 8; ++c) {
+              const uint32_t at = piece(c);
+              float f[8];
+              unpack8<E>(lds128(at), f);
+              st_shared_v4(at, make_uint4(Fp16::pack2(f[0] * up, f[1] * up),
+                                          Fp16::pack2(f[2] * up, f[3] * up),
+                                          Fp16::pack2(f[4] * up, f[5] * up),
+                                          Fp16::pack2(f[6] * up, f[7] * up)));
+            }
+            // the score scale's exponent: e2 - 13 in -113..114
+            q_exp[n & 1][i * 128 + ct] = uint8_t(e2 - 13 + 128);
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
+        return true;
+      };
+      if (nt == 0) {
+        ok = widen_q();
+        continue;
+      }
+      for (int j = 0; ok && j < nt; ++j) {
+        const int t = gt + j, rs = t % C::NRAW, rph = (t / C::NRAW) & 1, st = t & 1, ph = (t >> 1) & 1;
+        const int valid = min(C::N, w.tok_end - w.tok_begin - j * C::N);
+        // K: page scales, then the codes
+        ok = mbar_wait_warp(smem_u32(&bars.kr_full[rs]), rph, limit, &abort_flag) &&
+             (t < 2 || mbar_wait_warp(smem_u32(&bars.k_empty[st]), ph ^ 1, limit, &abort_flag));
+        if (!ok) break;
+        uint32_t lost = 0u;   // by 16 columns
+        {
+          const int page = lane * 16 / P;
+          const bool in = lane < C::NG && lane * 16 < valid;
+          const float2 s = in ? raw_scale[rs][page] : make_float2(1.f, 1.f);
+          const bool gone = in && s.x < 0.f;
+          lost = __ballot_sync(0xffffffffu, gone);
+          if (j == 0) ref = __shfl_sync(0xffffffffu, gone ? 1.f : s.y, 0);
+          if (ct < C::NG)     // the first warp writes them
+            scale_sh[t % kScaleRing][lane] =
+                make_float4(gone ? 0.f : s.x, gone ? 0.f : lg2(s.y),
+                            fminf(ref / s.y, 1.2676506e30f), ref);
+          if (ct == 0) lost_sh[t % kScaleRing] = int(lost);
+          if (ct < 32) {
+            __syncwarp();
+            if (ct == 0) mbar_arrive(smem_u32(&bars.sc_full[t % kScaleRing]));
+          }
+        }
+        widen(base + C::OFF_RAW + rs * C::RAW, base + C::OFF_K + st * C::KV, valid, lost);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars.kr_empty[rs]));
+          mbar_arrive(smem_u32(&bars.k_full[st]));
+        }
+        if (j == 0) {
+          ok = widen_q();
+          if (!ok) break;
+        }
+        ok = mbar_wait_warp(smem_u32(&bars.vr_full[rs]), rph, limit, &abort_flag) &&
+             (t < 2 || mbar_wait_warp(smem_u32(&bars.v_empty[st]), ph ^ 1, limit, &abort_flag));
+        if (!ok) break;
+        widen(base + C::OFF_RAW + (C::NRAW + rs) * C::RAW, base + C::OFF_V + st * C::KV, valid, lost);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars.vr_empty[rs]));
+          mbar_arrive(smem_u32(&bars.v_full[st]));
+        }
+      }
+      gt += nt;
+    }
+    if (!ok && lane == 0) fail();
+  } else if (warp >= C::W_MMA) {
+    setmaxnreg_dec<C::HELP_REGS>();
+    if (warp == C::W_KV) {
+      // -------------------------------------------------------------- K/V copies
+      if (lane == 0) {
+        prefetch_tensormap(&k_map);
+        prefetch_tensormap(&v_map);
+      }
+      const uint32_t box = uint32_t(P) * C::RAW_ROW;
+      auto publish = [&](int n, int value) {
+        if (n >= kItemRing &&
+            !mbar_wait_bounded(smem_u32(&bars.item_empty[n % kItemRing]),
+                               ((n / kItemRing) & 1) ^ 1, limit, &abort_flag))
+          return false;
+        item_ring[n % kItemRing] = value;
+        mbar_arrive(smem_u32(&bars.item_full[n % kItemRing]));
+        return true;
+      };
+      auto next_item = [&](int n, int& idx) {
+        int v = -1;
+        bool good = true;
+        if (lane == 0) {
+          v = n == 0 ? int(blockIdx.x) : int(gridDim.x + atomicAdd(prm.work_counter, 1u));
+          if (v >= prm.n_items) v = -1;
+          good = publish(n, v);
+        }
+        idx = __shfl_sync(0xffffffffu, v, 0);
+        return __shfl_sync(0xffffffffu, good, 0) != 0;
+      };
+      auto pages_in = [&](const WorkItem& w, int j) {
+        return (min(C::N, w.tok_end - w.tok_begin - j * C::N) + P - 1) / P;
+      };
+      int it = -1, t = 0;
+      bool ok = next_item(0, it);
+      WorkItem w;
+      if (ok && it >= 0) w = prm.items[it];
+      int next_page = -1;
+      if (ok && it >= 0 && tiles_of(w) > 0 && lane < pages_in(w, 0))
+        next_page = prm.page_indices[w.page_begin + lane];
+      for (int n = 0; ok && it >= 0; ++n) {
+        const int nt = tiles_of(w);
+        const int c1 = prm.layout == FI_LAYOUT_NHD ? w.head : 0;
+        const int c2 = prm.layout == FI_LAYOUT_NHD ? 0 : w.head;
+        int it_next = -1;
+        if (!next_item(n + 1, it_next)) {
+          ok = false;
+          break;
+        }
+        WorkItem wn;
+        if (it_next >= 0) wn = prm.items[it_next];
+        const bool more = it_next >= 0 && tiles_of(wn) > 0;
+        if (nt == 0)
+          next_page = more && lane < pages_in(wn, 0) ? prm.page_indices[wn.page_begin + lane] : -1;
+        for (int j = 0; j < nt; ++j, ++t) {
+          const int rs = t % C::NRAW, rph = (t / C::NRAW) & 1;
+          const int page = next_page;
+          const bool mine = lane < pages_in(w, j);
+          const bool valid = mine && page >= 0 && page < prm.num_pages;
+          if (mine && !valid) atomicOr(prm.err, kErrBounds);
+          next_page = -1;
+          if (j + 1 < nt) {
+            if (lane < pages_in(w, j + 1))
+              next_page = prm.page_indices[w.page_begin + (j + 1) * ppt + lane];
+          } else if (more && lane < pages_in(wn, 0)) {
+            next_page = prm.page_indices[wn.page_begin + lane];
+          }
+          const uint32_t bytes =
+              uint32_t(__popc(__ballot_sync(0xffffffffu, valid))) * C::RAW_BLK * box;
+          const bool skip = t == 0 && prm.fault_kind == 1 && blockIdx.x == 0;
+          const uint32_t kf = smem_u32(&bars.kr_full[rs]), vf = smem_u32(&bars.vr_full[rs]);
+          if (t >= C::NRAW && !mbar_wait_warp(smem_u32(&bars.kr_empty[rs]), rph ^ 1, limit,
+                                              &abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0 && !skip) mbar_arrive_expect_tx(kf, bytes);
+          __syncwarp();
+          if (valid && !skip) {
+            const uint32_t dst = base + C::OFF_RAW + rs * C::RAW + lane * box;
+#pragma unroll
+            for (int b = 0; b < C::RAW_BLK; ++b)
+              tma_load_4d(dst + b * C::N * 128, &k_map, kf, b * 128, c1, c2, page);
+          }
+          if (lane < ppt) {
+            if (valid) {
+              const size_t at = size_t(page) * hkv + w.head;
+              const uint32_t sc = smem_u32(&raw_scale[rs][lane]);
+              cp_async4(sc, prm.k_head_scale + at);
+              cp_async4(sc + 4, prm.v_head_scale + at);
+              cp_async_arrive(kf);
+            } else {
+              raw_scale[rs][lane] = make_float2(-1.f, 1.f);
+              mbar_arrive(kf);
+            }
+          }
+          issued = t + 1;
+          if (t >= C::NRAW && !mbar_wait_warp(smem_u32(&bars.vr_empty[rs]), rph ^ 1, limit,
+                                              &abort_flag)) {
+            ok = false;
+            issued = -issued;   // K of this tile, not V
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(vf, bytes);
+          __syncwarp();
+          if (valid) {
+            const uint32_t dst = base + C::OFF_RAW + (C::NRAW + rs) * C::RAW + lane * box;
+#pragma unroll
+            for (int b = 0; b < C::RAW_BLK; ++b)
+              tma_load_4d(dst + b * C::N * 128, &v_map, vf, b * 128, c1, c2, page);
+          }
+        }
+        w = wn;
+        it = it_next;
+      }
+      if (!ok && lane == 0) fail();
+      cp_async_wait_all();
+      __syncwarp();
+    } else if (warp == C::W_Q) {
+      // ---------------------------------------------------------------- Q copies
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        int it = -1;
+        ok = take_item(n, it);
+        if (!ok || it < 0) break;
+        const WorkItem w = prm.items[it];
+        if (n >= 1) ok = mbar_wait_warp(smem_u32(&bars.q_empty), (n - 1) & 1, limit, &abort_flag);
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t qb = smem_u32(&bars.q_raw);
+          mbar_arrive_expect_tx(qb, C::TILES * C::Q);
+#pragma unroll
+          for (int i = 0; i < C::TILES; ++i)
+#pragma unroll
+            for (int c = 0; c < C::DBLK; ++c)
+              tma_load_3d(base + C::OFF_Q + i * C::Q + c * C::M * 128, &q_map, qb, c * 64,
+                          w.head * g, w.q_row + i * R);
+        }
+        q_loads = n + 1;
+      }
+      if (!ok && lane == 0) fail();
+      __syncwarp();
+    } else if (warp < C::W_MMA + C::TILES) {
+      // ------------------------------------------------------------- MMA issuers
+      const int i = warp - C::W_MMA;
+      if (lane == 0) {
+        const uint64_t qd0 = sdesc_sw128(base + C::OFF_Q + i * C::Q, 16, 1024);
+        const uint64_t kd0 = sdesc_sw128(base + C::OFF_K, 16, 1024);
+        const uint64_t vd0 = sdesc_sw128(base + C::OFF_V, C::N * 128, 1024);
+        const uint32_t s_col = tmem + C::col_s(i), o_col = tmem + C::col_o(i);
+        auto wait = [&](uint64_t& bar, uint32_t parity) {
+          return mbar_wait_bounded(smem_u32(&bar), parity, limit, &abort_flag);
+        };
+        bool ok = true;
+        int t = 0;      // tiles of earlier items
+        int mine = 0;   // of which this issuer's tile took part in
+        for (int n = 0; ok; ++n) {
+          int it = -1;
+          ok = item_at(n, it);
+          item_done(n);
+          if (!ok || it < 0) break;
+          const WorkItem w = prm.items[it];
+          const int nt = tiles_of(w);
+          ok = wait(bars.q_full, n & 1);
+          if (!active(w, i)) {
+            // keeps the rings going: its share of each tile's release
+            for (int j = 0; ok && j < nt; ++j, ++t) {
+              ok = wait(bars.k_full[t & 1], (t >> 1) & 1);
+              if (ok) mbar_arrive(smem_u32(&bars.k_empty[t & 1]));
+              ok = ok && wait(bars.v_full[t & 1], (t >> 1) & 1);
+              if (ok) mbar_arrive(smem_u32(&bars.v_empty[t & 1]));
+            }
+            if (ok) mbar_arrive(smem_u32(&bars.q_empty));
+            continue;
+          }
+          for (int j = 0; ok && j < nt; ++j, ++t, ++mine) {
+            const int st = t & 1, ph = (t >> 1) & 1;
+            // (the K of later tiles was waited for while the previous tile's softmax ran)
+            if (j == 0) ok = wait(bars.k_full[st], ph);
+            // S and P share columns, and the softmax rescales O after S is
+            // full: the previous O += P V completes first
+            if (ok && mine >= 1) ok = wait(bars.pv_done[i], (mine - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kd = kd0 + uint64_t((st * C::KV) >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint64_t a = qd0 + uint64_t(((k >> 2) * C::M * 128 + (k & 3) * 32) >> 4);
+              const uint64_t b = kd + uint64_t(((k >> 2) * C::N * 128 + (k & 3) * 32) >> 4);
+              tc_mma_ss(s_col, a, b, C::IDESC_QK, k > 0 ? 1u : 0u);
+            }
+            tc_commit(smem_u32(&bars.s_full[i]));
+            tc_commit(smem_u32(&bars.k_empty[st]));
+            if (j == nt - 1) tc_commit(smem_u32(&bars.q_empty));
+            if (j + 1 < nt) ok = wait(bars.k_full[st ^ 1], ((t + 1) >> 1) & 1);
+            if (ok) ok = wait(bars.v_full[st], ph);
+            if (ok) ok = wait(bars.p_full[i], mine & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = vd0 + uint64_t((st * C::KV) >> 4);
+#pragma unroll
+            for (int k = 0; k < C::N / 16; ++k)
+              tc_mma_ts(o_col, s_col + k * 8, vd + uint64_t((k * 16 * 128) >> 4), C::IDESC_PV,
+                        (j > 0 || k > 0) ? 1u : 0u);
+            tc_commit(smem_u32(&bars.v_empty[st]));
+            tc_commit(smem_u32(&bars.pv_done[i]));
+          }
+          if (!ok) break;
+          if (nt == 0) tc_commit(smem_u32(&bars.q_empty));
+          else tc_commit(smem_u32(&bars.o_final[i]));
+        }
+        if (!ok) fail();
+        // every MMA issued so far completes before the TMEM is released
+        tc_commit(smem_u32(&bars.drain[i]));
+        mbar_wait_bounded(smem_u32(&bars.drain[i]), 0, limit, nullptr);
+      }
+      __syncwarp();
+    }
+  } else {
+    setmaxnreg_inc<C::SOFT_REGS>();
+    // ------------------------------------------------------- softmax + epilogue
+    const int i = warp >> 2;
+    const int t = (warp & 3) * 32 + lane;             // M row of the tile = TMEM lane
+    const int row_in = i * R + t / g;                 // query row within the item
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lane_off + C::col_s(i);
+    const uint32_t o_col = tmem + lane_off + C::col_o(i);
+    const float scale0 = prm.sm_scale * kLog2e;
+    bool ok = true;
+    int gt = 0;      // tiles of earlier items
+    int mine = 0;    // of which this tile took part in
+    int shared = 0;  // and of which both did
+    int outs = 0;    // items with keys this tile took part in
+    for (int n = 0; ok; ++n) {
+      int it = -1;
+      ok = take_item(n, it);
+      if (!ok || it < 0) break;
+      const WorkItem w = prm.items[it];
+      const int nt = tiles_of(w);
+      const bool both = C::TILES == 2 && active(w, 1);
+      if (i == 1 && !both) {
+        gt += nt;
+        continue;
+      }
+      const int q_start = prm.qo_indptr[w.req], q_end = prm.qo_indptr[w.req + 1];
+      const int np_req = prm.page_indptr[w.req + 1] - prm.page_indptr[w.req];
+      const int kv_len = np_req > 0 ? (np_req - 1) * P + prm.last_page_len[w.req] : 0;
+      const int q_row = w.q_row + row_in;
+      const int pos = kv_len - (q_end - q_start) + (q_row - q_start);   // key position
+      const int t_max = min(prm.causal ? pos : kv_len - 1, kv_len - 1);
+      const int t_min = prm.window_left >= 0 ? pos - prm.window_left : INT_MIN;
+      float unit = scale0;   // the row's score scale (the page's s_k joins it)
+      float ref = 1.f;       // r
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < nt; ++j, ++gt, ++mine) {
+        // The tiles' warpgroups take turns, so that one softmax runs while the
+        // tensor core works on the other tile.
+        bool turn = true;
+        if (both)
+          turn = i == 1 ? mbar_wait_warp(smem_u32(&bars.turn[0]), shared & 1, limit, &abort_flag)
+                        : (shared == 0 || mbar_wait_warp(smem_u32(&bars.turn[1]), (shared - 1) & 1,
+                                                         limit, &abort_flag));
+        if (!turn || !mbar_wait_warp(smem_u32(&bars.sc_full[gt % kScaleRing]),
+                                     (gt / kScaleRing) & 1, limit, &abort_flag) ||
+            !mbar_wait_warp(smem_u32(&bars.s_full[i]), mine & 1, limit, &abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (j == 0) {
+          // (the first scores are there, so the widened q and its exponents
+          // are. Waiting for q_full itself here would be wrong: where items
+          // have one K tile, q_full runs on to the next item's phase while
+          // this warp is still in the previous item's epilogue)
+          if constexpr (kWidenQ) {
+            const int e = int(q_exp[n & 1][i * 128 + t]) - 128;
+            unit *= __uint_as_float(uint32_t(127 + e) << 23);
+          }
+          ref = scale_sh[gt % kScaleRing][0].w;
+        }
+        const int col0 = w.tok_begin + j * C::N;
+        const int hi = t_max - col0;
+        const int lo = t_min > col0 ? t_min - col0 : 0;
+        const uint32_t lost = uint32_t(lost_sh[gt % kScaleRing]);
+        const float4* sc = scale_sh[gt % kScaleRing];
+        const bool need_mask = __any_sync(0xffffffffu, hi < C::N - 1 || lo > 0) || lost != 0u;
+        auto body = [&](auto masked) {
+          constexpr bool MK = decltype(masked)::value;
+          uint32_t sr[C::N / 32][32];
+#pragma unroll
+          for (int c = 0; c < C::N / 32; ++c) tmem_ld32(s_col + c * 32, sr[c]);
+          tmem_wait_ld();
+          if (MK) {
+#pragma unroll
+            for (int k = 0; k < C::N; ++k)
+              if (k > hi || k < lo || ((lost >> (k >> 4)) & 1u)) sr[k >> 5][k & 31] = 0xff800000u;
+          }
+          // s + log2 s_v of a group's largest score; the scale is at least
+          // FLT_MIN (a hidden score is -inf, and -inf * 0 would be NaN)
+          float cu[C::NG], lv[C::NG];
+          float m_tile = -INFINITY;
+#pragma unroll
+          for (int p = 0; p < C::NG; ++p) {
+            const float2 s = *reinterpret_cast<const float2*>(sc + p);
+            cu[p] = fmaxf(s.x * unit, FLT_MIN);
+            lv[p] = s.y;
+            float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const int k = p * 16 + e;
+              a = fmax3(a, __uint_as_float(sr[k >> 5][k & 31]),
+                        __uint_as_float(sr[k >> 5][(k + 1) & 31]));
+              b = fmax3(b, __uint_as_float(sr[k >> 5][(k + 2) & 31]),
+                        __uint_as_float(sr[k >> 5][(k + 3) & 31]));
+            }
+            m_tile = fmaxf(m_tile, fmaf(fmaxf(a, b), cu[p], lv[p]));
+          }
+          const float m_new = fmaxf(m, m_tile);
+          const bool grow = m_new > m + kRescaleThreshold;
+          const bool o_live = grow && m != -INFINITY;
+          float alpha = 1.f;
+          if (grow) {
+            alpha = ex2(m - m_new);
+            l *= alpha;
+            m = m_new;
+          }
+          // O is settled: this S was issued after the previous O += P V had completed
+          if (__any_sync(0xffffffffu, o_live)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t r[16];
+              tmem_ld16(o_col + c * 16, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+              tmem_st16(o_col + c * 16, r);
+            }
+            tmem_wait_st();
+          }
+          const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int p = 0; p < C::NG; p += 2) {
+            uint32_t wv[16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float b = lv[p + h] - mm;
+              const float2 c2 = make_float2(cu[p + h], cu[p + h]), b2 = make_float2(b, b);
+              float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const int k = (p + h) * 16 + e;
+                const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[k >> 5][k & 31]),
+                                                        __uint_as_float(sr[k >> 5][(k + 1) & 31])),
+                                            c2, b2);
+                const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                sum = __fadd2_rn(sum, y);
+                wv[h * 8 + e / 2] = Fp16::pack2(y.x, y.y);
+              }
+              l = fmaf(sum.x + sum.y, sc[p + h].z, l);
+            }
+            tmem_st16(s_col + p * 8, wv);
+          }
+          tmem_wait_st();
+        };
+        if (need_mask) body(std::true_type{});
+        else body(std::false_type{});
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars.p_full[i]));
+          if (both) mbar_arrive(smem_u32(&bars.turn[i]));
+        }
+        shared += both ? 1 : 0;
+      }
+      if (!ok) break;
+      if (nt > 0) {
+        if (!mbar_wait_warp(smem_u32(&bars.o_final[i]), outs & 1, limit, &abort_flag)) {
+          ok = false;
+          break;
+        }
+        ++outs;
+      }
+      tc_fence_after();
+      // ---- epilogue (a piece of a split item writes the rows' fp32 states)
+      const bool row_ok = q_row < q_end;
+      const float inv = l == 0.f ? 0.f : prm.v_scale * ref / l;
+      const int head = w.head * g + t % g;
+      const bool piece = w.merge > 0;
+      const size_t orow = piece ? size_t(w.slot) + size_t(row_in) * size_t(w.merge) : size_t(q_row);
+      const size_t at = orow * prm.num_qo_heads + head;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        if (nt > 0) {
+          tmem_ld32(o_col + c * 32, r);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = 0u;
+        }
+        const float* f = reinterpret_cast<const float*>(r);
+        if (row_ok && piece) {
+          float4* dst = reinterpret_cast<float4*>(prm.piece_o + at * D + c * 32);
+#pragma unroll
+          for (int q4 = 0; q4 < 8; ++q4)
+            dst[q4] = make_float4(f[q4 * 4] * inv, f[q4 * 4 + 1] * inv, f[q4 * 4 + 2] * inv,
+                                  f[q4 * 4 + 3] * inv);
+        } else if (row_ok) {
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(prm.out) + at * D + c * 32);
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const float* x = f + q4 * 8;
+            dst[q4] = make_uint4(E::pack2(x[0] * inv, x[1] * inv), E::pack2(x[2] * inv, x[3] * inv),
+                                 E::pack2(x[4] * inv, x[5] * inv), E::pack2(x[6] * inv, x[7] * inv));
+          }
+        }
+      }
+      float* lse = piece ? prm.piece_lse : prm.lse;
+      if (row_ok && lse) lse[at] = l == 0.f ? -INFINITY : (m + (lg2(l) - lg2(ref))) * kLn2;
+      tc_fence_before();
+    }
+    if (!ok && lane == 0) fail();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::W_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+  // every copy that was issued lands before the CTA exits, also after a timeout
+  if (warp == C::W_KV && lane == 0) {
+    const bool no_v = issued < 0;   // of the last tile
+    if (no_v) issued = -issued;
+    for (int j = max(0, issued - C::NRAW); j < issued; ++j) {
+      if (!(j == 0 && prm.fault_kind == 1 && blockIdx.x == 0))   // K never issued
+        mbar_wait_bounded(smem_u32(&bars.kr_full[j % C::NRAW]), (j / C::NRAW) & 1, limit, nullptr);
+    }
+    const int nv = no_v ? issued - 1 : issued;
+    for (int j = max(0, nv - C::NRAW); j < nv; ++j)
+      mbar_wait_bounded(smem_u32(&bars.vr_full[j % C::NRAW]), (j / C::NRAW) & 1, limit, nullptr);
+  }
+  if (warp == C::W_Q && lane == 0 && q_loads > 0)
+    mbar_wait_bounded(smem_u32(&bars.q_raw), (q_loads - 1) & 1, limit, nullptr);
+}
+
+template <int D, class E>
+cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
+                     const PrefillParams& p, int grid, cudaStream_t stream) {
+  using C = P8Cfg<D>;
+  auto kern = prefill_page8_kernel<D, E>;
+  static std::atomic<uint64_t> configured{0};
+  const cudaError_t e = once_per_device(configured, [&] {
+    // the warpgroups' register split assumes this launch allocation
+    cudaFuncAttributes fa;
+    cudaError_t r = cudaFuncGetAttributes(&fa, kern);
+    if (r != cudaSuccess) return r;
+    if (fa.numRegs != int(C::LAUNCH_REGS)) return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  });
+  if (e != cudaSuccess) return e;
+  kern<<<grid, C::THREADS, C::SMEM, stream>>>(qm, km, vm, p);
+  return cudaGetLastError();
+}
+
+template <class E>
+cudaError_t launch_d(int head_dim, const CUtensorMap& qm, const CUtensorMap& km,
+                     const CUtensorMap& vm, const PrefillParams& p, int grid, cudaStream_t stream) {
+  switch (head_dim) {
+    case 64: return launch_t<64, E>(qm, km, vm, p, grid, stream);
+    case 128: return launch_t<128, E>(qm, km, vm, p, grid, stream);
+    case 256: return launch_t<256, E>(qm, km, vm, p, grid, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_page8(int head_dim, int dtype, const CUtensorMap& qm,
+                                 const CUtensorMap& km, const CUtensorMap& vm,
+                                 const PrefillParams& p, int num_sms, cudaStream_t stream) {
+  const int grid = p.n_items < num_sms ? p.n_items : num_sms;
+  if (grid <= 0) return cudaSuccess;
+  switch (dtype) {
+    case FI_DTYPE_BF16: return launch_d<Bf16>(head_dim, qm, km, vm, p, grid, stream);
+    case FI_DTYPE_FP16: return launch_d<Fp16>(head_dim, qm, km, vm, p, grid, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace fi

@@ -211,3 +211,203 @@ def test_decode_on_another_stream():
         d.run()
     s.synchronize()
     assert torch.equal(d.out, o1)
+
+
+# ---- prefill -----------------------------------------------------------------------------------
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("g", [1, 2, 4, 8])
+@pytest.mark.parametrize("layout,P,dtype", [("NHD", 16, "bf16"), ("HND", 32, "fp16")])
+def test_prefill_shapes(d, g, layout, P, dtype):
+    """Whole prompts, chunks on earlier keys, a few rows, single rows, empty
+    requests; row counts that end inside a tile and at its edge."""
+    kv = [5, 300, 1, 0, 129, 70, 700, 64, 257, 33]
+    qo = [5, 300, 1, 0, 1, 3, 130, 33, 257, 0]
+    b = _page8.Batch(kv, 2 * g, 2, d, P, layout, dtype, qo_lens=qo, seed=d + g, tail=0x7f)
+    _check(b, what=f"d{d} g{g} {layout} {dtype}")
+
+
+@pytest.mark.parametrize("g,d", [(8, 128), (1, 64), (2, 256)])
+def test_prefill_not_causal(g, d):
+    b = _page8.Batch([40, 0, 300, 129], 2 * g, 2, d, 16, qo_lens=[70, 4, 9, 1], causal=False, seed=21,
+                     tail=0xff)
+    _check(b, what="full")
+
+
+@pytest.mark.parametrize("sms", [1, 152, 2000])
+@pytest.mark.parametrize("g,d", [(8, 128), (4, 64), (2, 256)])
+def test_prefill_splits(sms, g, d):
+    b = _page8.Batch([5000, 3000, 900], 2 * g, 2, d, 16, qo_lens=[60, 7, 140], seed=22)
+    assert (B.fi_plan_get_info(b.plan(B, sms))["num_partial_slots"] > 0) == (sms > 1)
+    _check(b, sms, what=f"sms {sms}")
+
+
+@pytest.mark.parametrize("w", [0, 1, 16, 100, 127, 128, 1000])
+@pytest.mark.parametrize("g,d", [(8, 128), (1, 64), (4, 256)])
+def test_prefill_window(w, g, d):
+    b = _page8.Batch([333, 40, 900], 2 * g, 2, d, 16, qo_lens=[333, 3, 50], window=w, seed=w)
+    _check(b, what=f"window {w}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("g,d", [(8, 128), (1, 128), (4, 64), (2, 256)])
+def test_prefill_any_scales(g, d, dtype):
+    kv, qo = [900, 33, 257], [40, 33, 200]
+    b = _page8.Batch(kv, 2 * g, 2, d, 16, dtype=dtype, qo_lens=qo, seed=3, scales="any")
+    _check(b, what="any", k_scale=0.5, v_scale=3.0)
+    b = _page8.Batch(kv, 2 * g, 2, d, 32, qo_lens=qo, seed=4, v_spread=12)
+    _check(b, what="spread")
+
+
+def test_prefill_small_scale_pages_keep_their_weight():
+    import torch
+    b = _page8.Batch([64], 8, 1, 128, 16, qo_lens=[16], seed=5)
+    b.codes[0][:] = 0x38
+    for s in b.scale:
+        s[:] = 1.0
+    b.scale[0][b.page_indices[2], 0] = 64.0
+    b.scale[1][b.page_indices[2], 0] = 2.0 ** -40
+    b.q = torch.ones_like(b.q)
+    _check(b, what="small page")
+
+
+def test_prefill_q_range_and_special_values():
+    import torch
+    for dtype, lo in (("bf16", -30), ("fp16", -12)):
+        b = _page8.Batch([200, 90], 4, 1, 128, 16, dtype=dtype, qo_lens=[30, 40], seed=6)
+        e = torch.from_numpy(np.random.default_rng(1).integers(lo, 1, (70, 4, 128)))
+        b.q = (b.q.double() * torch.exp2(e.double())).to(b.q.dtype)
+        b.q[1] = 0
+        _check(b, what=f"range {dtype}")
+        b.q[2, 1, 5] = float("nan")
+        b.q[50, 2, 7] = float("inf")
+        d = _page8.Device(b)
+        out, lse = d.run()
+        want = np.zeros((70, 4), dtype=bool)
+        want[2, 1] = want[50, 2] = True
+        assert np.array_equal(torch.isnan(out).all(dim=2).cpu().numpy(), want)
+        assert np.array_equal(torch.isnan(out).any(dim=2).cpu().numpy(), want)
+        assert np.array_equal(torch.isnan(lse).cpu().numpy(), want)
+
+
+def test_prefill_deterministic_rows_behind_stay():
+    import torch
+    b = _page8.Batch([3000, 500, 900], 16, 2, 128, 16, qo_lens=[300, 2, 77], seed=9)
+    d = _page8.Device(b)
+    out = torch.full((b.rows + 5, 16, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    d.out = out[:b.rows]
+    o1, l1 = [x.clone() for x in d.run()]
+    assert bool((out[b.rows:] == 7).all())
+    for _ in range(3):
+        d.out.fill_(7)
+        o2, l2 = d.run()
+        assert torch.equal(o1, o2) and torch.equal(l1, l2)
+
+
+def test_prefill_page_outside_the_cache_is_skipped_and_reported():
+    b = _page8.Batch([200, 60], 8, 2, 128, 16, qo_lens=[20, 10], seed=11)
+    d = _page8.Device(b)
+    want = _page8.reference(b)
+    d.page_indices[2] = b.num_pages
+    d.page_indices[3] = -1
+    out, lse = d.run()
+    assert d.status() == B.FI_ERR_DEVICE_BOUNDS
+    _page8.compare(b, out, lse, want, rows=np.arange(20, 30), what="other request")
+    q, k, v = b.q64(), b.kv64(0), b.kv64(1)
+    for i in (0, 19):
+        t = np.array([x for x in range(181 + i) if x // 16 not in (2, 3)])
+        pages = b.page_indices[t // 16]
+        for h in (0, 7):
+            s = b.sm_scale * (k[pages, t % 16, h // 4] @ q[i, h])
+            p = np.exp(s - s.max())
+            o = p @ v[pages, t % 16, h // 4] / p.sum()
+            assert np.abs(out[i, h].double().cpu().numpy() - o).max() < 2e-2
+            assert abs(lse[i, h].item() - (s.max() + np.log(p.sum()))) < 1e-4
+    d.page_indices[2], d.page_indices[3] = int(b.page_indices[2]), int(b.page_indices[3])
+    _page8.compare(b, *d.run(), want, what="after")
+    assert d.status() == B.FI_OK
+
+
+@pytest.mark.parametrize("d,g", [(128, 8), (64, 1), (256, 4)])
+def test_prefill_bounded_wait_and_recovery(d, g):
+    b = _page8.Batch([300, 40, 1000], 2 * g, 2, d, 16, qo_lens=[100, 2, 1], seed=12)
+    dv = _page8.Device(b)
+    B.fi_debug_set_fault(1, 50_000_000)
+    try:
+        dv.run()
+        assert dv.status() == B.FI_ERR_DEVICE_TIMEOUT
+    finally:
+        B.fi_debug_set_fault(0, 0)
+    _page8.compare(b, *dv.run(), _page8.reference(b), what="after")
+    assert dv.status() == B.FI_OK
+
+
+def test_prefill_through_host_buffers():
+    import torch
+    b = _page8.Batch([500, 3, 0, 64], 8, 2, 128, 16, qo_lens=[200, 3, 0, 1], seed=13)
+    d = _page8.Device(b)
+    o1, l1 = [x.clone() for x in d.run()]
+    info = B.fi_plan_get_info(d.plan)
+    ws = torch.empty(info["workspace_bytes"] + info["host_io_bytes"], dtype=torch.uint8, device="cuda")
+    oh, lh = torch.empty(o1.shape, dtype=o1.dtype), torch.empty(l1.shape)
+    B.fi_batch_attention_host(d.plan, b.q.contiguous(), b.qo_indptr, d.k, d.v, B.FI_LAYOUT_NHD, 0,
+                              b.num_pages, b.page_indptr, b.page_indices, b.last_page_len,
+                              b.sm_scale, 1.0, 1.0, oh, lh, ws, ws.numel(), k_head_scale=d.ks,
+                              v_head_scale=d.vs)
+    assert torch.equal(oh, o1.cpu()) and torch.equal(lh, l1.cpu())
+
+
+@pytest.mark.parametrize("g,d,dtype", [(8, 128, "bf16"), (2, 64, "bf16"), (4, 256, "fp16"),
+                                       (1, 128, "fp16")])
+def test_prefill_many_items_of_few_keys(g, d, dtype):
+    """Thousands of items with one K/V tile or none, next to each other, with
+    one and with two row tiles: the pipeline's phases move from item to item
+    with nothing in between. Every pass ends, without a wait that ran out, and
+    gives the same bits."""
+    import torch
+    rng = np.random.default_rng(31)
+    kv = rng.integers(1, 129, 300)
+    kv[::7] = rng.integers(100, 300, len(kv[::7]))
+    qo = np.minimum(kv, rng.integers(2, 2 * 256 // g, 300))
+    b = _page8.Batch(kv, 8 * g, 8, d, 16, dtype=dtype, qo_lens=qo, seed=31)
+    dv = _page8.Device(b)
+    o1, l1 = [x.clone() for x in dv.run()]
+    some = [0, 7, 50, 299]
+    rows = np.concatenate([np.arange(b.qo_indptr[r], b.qo_indptr[r + 1]) for r in some])
+    _page8.compare(b, o1, l1, _page8.reference(b, some), rows=rows, what="some")
+    assert dv.status() == B.FI_OK
+    for _ in range(100):
+        dv.run()
+        assert torch.equal(dv.out, o1) and torch.equal(dv.lse, l1)
+        assert dv.status() == B.FI_OK
+
+
+def test_prefill_many_items_without_keys():
+    """Rows of requests without keys between others (not causal): zeros."""
+    import torch
+    kv = [0, 0, 50, 0, 0, 0, 300, 0] * 20
+    b = _page8.Batch(kv, 8, 2, 128, 16, qo_lens=[3, 70, 5, 9, 2, 200, 40, 2] * 20, causal=False, seed=32)
+    dv = _page8.Device(b)
+    o1, l1 = [x.clone() for x in dv.run()]
+    _page8.compare(b, o1, l1, _page8.reference(b), what="empty")
+    for _ in range(50):
+        dv.run()
+        assert torch.equal(dv.out, o1) and dv.status() == B.FI_OK
+
+
+@pytest.mark.parametrize("g,d,dtype", [(8, 128, "bf16"), (1, 64, "bf16"), (4, 256, "fp16")])
+def test_decode_many_items_of_few_keys(g, d, dtype):
+    """Thousands of items with one tile, a few or none next to each other: the
+    same bits in every pass, and no wait that ran out."""
+    import torch
+    rng = np.random.default_rng(33)
+    kv = rng.integers(0, 130, 700)
+    kv[::9] = rng.integers(100, 700, len(kv[::9]))
+    b = _page8.Batch(kv, 4 * g, 4, d, 16, dtype=dtype, seed=33)
+    dv = _page8.Device(b)
+    o1, l1 = [x.clone() for x in dv.run()]
+    some = [0, 9, 50, 699]
+    _page8.compare(b, o1, l1, _page8.reference(b, some), rows=np.array(some), what="some")
+    for _ in range(100):
+        dv.run()
+        assert torch.equal(dv.out, o1) and torch.equal(dv.lse, l1)
+        assert dv.status() == B.FI_OK
