@@ -478,13 +478,12 @@ fi_status run_paged(fi_plan_t plan, bool prefill_call, const void* q, const int3
   float* partial_lse = reinterpret_cast<float*>(ws + P.ws.partial_lse);
 
   CUtensorMap qmap;
-  if (!P.prefill_items.empty() || !P.prefix_items.empty()) {
-    // prefill tiles hold 128 rows of one head; shared-prefix tiles, and all
-    // tiles over a page-scaled cache, 128 / g rows of the g heads of a kv
-    // head (a decode plan has only the former of these)
+  if ((!P.prefill_items.empty() || !P.prefix_items.empty()) && !page8) {
+    // prefill tiles hold 128 rows of one head; shared-prefix tiles 128 / g
+    // rows of the g heads of a kv head (a decode plan has only the latter)
     st = q_map(&qmap, q, P.total_q, P.num_qo_heads,
-                    P.prefix_items.empty() && !page8 ? 1 : P.num_qo_heads / P.num_kv_heads,
-                    P.head_dim, P.dtype);
+                    P.prefix_items.empty() ? 1 : P.num_qo_heads / P.num_kv_heads, P.head_dim,
+                    P.dtype);
     if (st != FI_OK) return st;
   }
 
@@ -585,7 +584,7 @@ fi_status run_paged(fi_plan_t plan, bool prefill_call, const void* q, const int3
       dstream = side.stream;
     }
     if (!P.prefill_items.empty()) {
-      e = page8 ? fi::launch_prefill_page8(P.head_dim, P.dtype, qmap, kmap, vmap, pp, P.num_sms,
+      e = page8 ? fi::launch_prefill_page8(P.head_dim, P.dtype, q, kmap, vmap, pp, P.num_sms,
                                            stream)
                 : fi::launch_prefill(P.head_dim, P.dtype, qmap, kmap, vmap, pp, P.num_sms, stream);
       if (e != cudaSuccess) return cuda_fail(e, "prefill launch");

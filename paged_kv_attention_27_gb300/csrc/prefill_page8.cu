@@ -6,12 +6,17 @@
 // inner, so that every K/V tile that is loaded serves all of them; a draft's
 // few rows and a long prompt run the same way.
 //
-// Arithmetic: codes are exact in fp16, so both products run as fp16 tcgen05
-// MMAs (fp32 accumulators in TMEM) on tiles that a warpgroup widens from the
-// cache bytes. A bf16 q row is widened too: times the power of two that puts
-// its largest element at 2^13..2^14, exact down to 2^-37 of that element; fp16
-// q enters as it is. The page's s_k joins the row's score scale, one factor per
-// 16 columns. The page's s_v joins the weight before it is rounded to fp16:
+// Arithmetic: the scores' MMAs take the K codes as they arrive (kind::f8f6f4).
+// A q row, times the power of two that puts its largest element at 224..448,
+// enters as a sum of e4m3 terms t0 = e4m3(x), t1 = e4m3(x - t0), ...: two carry
+// the 8 significand bits of bf16, three the 11 of fp16, down to E4M3's finest
+// step of 2^-9, so that an element is off by at most 2^-10, 2^-17 of the row's
+// largest. Two e4m3 MMAs cost what one 16-bit MMA would, and K is neither
+// widened nor stored twice. The outputs' MMAs multiply fp16 weights by V codes
+// that a warpgroup widens to fp16, exactly (splitting the weights instead would
+// cost the softmax warps three times the instructions that widening costs).
+// The page's s_k joins the row's score scale, one factor per 16 columns. The
+// page's s_v joins the weight before it is rounded to fp16:
 //   w = 2^(s + log2 s_v - m),  m the running maximum of s + log2 s_v,
 //   O = sum w code,  l = sum w r / s_v (r: s_v of the item's first page),
 //   out = O r / l,   lse = ln 2 (m + log2 l - log2 r):
@@ -21,10 +26,8 @@
 // Roles (TILES = 2: 16 warps; TILES = 1: 12): a softmax warpgroup per tile
 // (thread = M row = TMEM lane; they take turns so that one tile's MMAs run
 // under the other's softmax), then the epilogue; a warp each to issue a tile's
-// MMAs, to copy K/V pages and their scales, to copy Q; a warpgroup to widen.
-// Bound: tensor cores and the exponentials (16 per cycle), which at head_dim
-// 128 take the same time; widening costs 2 / 256 of the MMA work's
-// instructions' worth per row and runs beside both.
+// MMAs and one to copy K/V pages and their scales; a warpgroup to turn q into
+// terms and widen V.
 #include <cfloat>
 #include <climits>
 #include <type_traits>
@@ -50,47 +53,52 @@ constexpr int kItemRing = 8;
 // is complete, which was issued after the softmax of tile t - 3
 constexpr int kScaleRing = 4;
 
-template <int D>
+template <int D, class E>
 struct P8Cfg {
   static constexpr int TILES = D <= 128 ? 2 : 1;
+  static constexpr int TERMS = std::is_same<E, Bf16>::value ? 2 : 3;
   static constexpr int M = 128;
   static constexpr int N = D <= 128 ? 128 : 64;             // keys per tile
   static constexpr int NG = N / 16;                         // 16-column groups (pages) of a tile
-  static constexpr int DBLK = D / 64;                       // 128-byte slices of an fp16 row
-  static constexpr int RAW_ROW = D < 128 ? D : 128;         // bytes of a row of codes
-  static constexpr int RAW_BLK = D <= 128 ? 1 : D / 128;
-  static constexpr int RAW = N * D;                         // one K (or V) tile of codes
-  static constexpr int NRAW = D == 64 ? 2 : 1;              // code tiles of K (and of V) in flight
-  static constexpr int KV = N * D * 2;                      // one widened tile
-  static constexpr int Q = M * D * 2;
+  static constexpr int ROWB = D < 128 ? D : 128;            // bytes of a shared-memory row of codes
+  static constexpr int BLK = D <= 128 ? 1 : D / 128;        // 128-byte slices of a row of codes
+  static constexpr uint32_t SWZ = ROWB == 128 ? 2 : 4;      // 128- or 64-byte swizzle
+  static constexpr uint32_t ATOM = 8 * ROWB;
+  static constexpr int CODES = N * D;                       // one K (or V) tile of codes
+  static constexpr int V = N * D * 2;                       // one widened V tile
+  static constexpr int QT = M * D;                          // one term of a tile's q
+  static constexpr int Q = TERMS * QT;
+  static constexpr int NK = 3;                              // K tiles in flight
+  static constexpr int NVR = TERMS == 3 && D >= 128 ? 1 : 2;   // V code tiles in flight
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + TILES * Q;           // two
-  static constexpr int OFF_V = OFF_K + 2 * KV;              // two
-  static constexpr int OFF_RAW = OFF_V + 2 * KV;            // K tiles, then V tiles
-  static constexpr int USED = OFF_RAW + 2 * NRAW * RAW;
+  static constexpr int OFF_K = OFF_Q + TILES * Q;
+  static constexpr int OFF_V = OFF_K + NK * CODES;          // two
+  static constexpr int OFF_VR = OFF_V + 2 * V;
+  static constexpr int USED = OFF_VR + NVR * CODES;
   static constexpr int SMEM = (USED < 120 * 1024 ? 120 * 1024 : USED) + 1024;   // one CTA per SM
+  static_assert(SMEM <= 226 * 1024, "shared-memory budget");
   static constexpr int SOFT = 4 * TILES;                    // softmax warps
-  static constexpr int W_MMA = SOFT, W_KV = SOFT + 2, W_Q = SOFT + 3, W_WIDE = SOFT + 4;
+  static constexpr int W_MMA = SOFT, W_KV = SOFT + 2, W_WIDE = SOFT + 4;
   static constexpr int THREADS = 32 * (SOFT + 8);
   // registers per thread at launch and, per warpgroup, after the split
   static constexpr uint32_t LAUNCH_REGS = TILES == 2 ? 128 : 168;
-  static constexpr uint32_t SOFT_REGS = TILES == 2 ? 192 : 240;
+  static constexpr uint32_t SOFT_REGS = TILES == 2 ? 184 : 240;
   static constexpr uint32_t HELP_REGS = TILES == 2 ? 56 : 104;
-  static constexpr uint32_t WIDE_REGS = TILES == 2 ? 72 : 160;
+  static constexpr uint32_t WIDE_REGS = TILES == 2 ? 88 : 160;
   static_assert(TILES * SOFT_REGS + HELP_REGS + WIDE_REGS <= (TILES + 2) * LAUNCH_REGS, "");
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t col_s(int i) { return uint32_t(i * N); }
   __host__ __device__ static constexpr uint32_t col_o(int i) { return uint32_t(TILES * N + i * D); }
   static_assert(TILES * (N + D) <= 512, "TMEM budget");
-  static constexpr uint32_t IDESC_QK = idesc_f16kind(M, N, 0, 0, Fp16::kMmaFmt);
+  static constexpr uint32_t IDESC_QK = idesc_e4m3(M, N, 0, 0);
   static constexpr uint32_t IDESC_PV = idesc_f16kind(M, D, 0, 1, Fp16::kMmaFmt);
 };
 
 struct P8Barriers {
   uint64_t item_full[kItemRing], item_empty[kItemRing];
-  uint64_t q_raw, q_full, q_empty;
-  uint64_t kr_full[2], kr_empty[2], vr_full[2], vr_empty[2];   // code tiles
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];       // widened tiles
+  uint64_t q_full, q_empty;
+  uint64_t k_full[3], k_empty[3], vr_full[2], vr_empty[2];     // tiles of codes
+  uint64_t v_full[2], v_empty[2];                              // widened tiles
   uint64_t s_full[2], p_full[2], pv_done[2], o_final[2], drain[2];
   uint64_t sc_full[kScaleRing];                                // a tile's page scales
   uint64_t turn[2];                                            // the softmax warpgroups' turns
@@ -103,18 +111,16 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
 }
 
 template <int D, class E>
-__global__ void __launch_bounds__(P8Cfg<D>::THREADS, 1)
-prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
-                     const __grid_constant__ CUtensorMap k_map,
+__global__ void __launch_bounds__(P8Cfg<D, E>::THREADS, 1)
+prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map, PrefillParams prm) {
-  using C = P8Cfg<D>;
-  constexpr bool kWidenQ = std::is_same<E, Bf16>::value;
+  using C = P8Cfg<D, E>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) P8Barriers bars;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ int item_ring[kItemRing];
-  __shared__ __align__(8) float2 raw_scale[2][8];           // per page of a code tile: s_k, s_v
+  __shared__ __align__(8) float2 raw_scale[C::NK][8];       // per page of a K tile: s_k, s_v
   __shared__ __align__(16) float4 scale_sh[kScaleRing][8];  // per 16 columns: s_k (-1: no page),
                                                             // log2 s_v, r / s_v, r
   __shared__ int lost_sh[kScaleRing];                       // the tile has a page outside the cache
@@ -160,19 +166,18 @@ prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
   if (threadIdx.x == 0) {
     for (int s = 0; s < kItemRing; ++s) {
       mbar_init(smem_u32(&bars.item_full[s]), 1);
-      // softmax warps, MMA warps, the Q warp, the widening warps
-      mbar_init(smem_u32(&bars.item_empty[s]), C::SOFT + C::TILES + 1 + 4);
+      // softmax warps, MMA warps, the widening warps
+      mbar_init(smem_u32(&bars.item_empty[s]), C::SOFT + C::TILES + 4);
     }
-    mbar_init(smem_u32(&bars.q_raw), 1);
     mbar_init(smem_u32(&bars.q_full), 4);
     mbar_init(smem_u32(&bars.q_empty), C::TILES);
+    for (int s = 0; s < C::NK; ++s) {
+      mbar_init(smem_u32(&bars.k_full[s]), 1 + ppt);        // the bytes, and each page's scales
+      mbar_init(smem_u32(&bars.k_empty[s]), C::TILES + 4);  // S of the tiles; the scales' readers
+    }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&bars.kr_full[s]), 1 + ppt);       // the bytes, and each page's scales
-      mbar_init(smem_u32(&bars.kr_empty[s]), 4);
       mbar_init(smem_u32(&bars.vr_full[s]), 1);
       mbar_init(smem_u32(&bars.vr_empty[s]), 4);
-      mbar_init(smem_u32(&bars.k_full[s]), 4);
-      mbar_init(smem_u32(&bars.k_empty[s]), C::TILES);
       mbar_init(smem_u32(&bars.v_full[s]), 4);
       mbar_init(smem_u32(&bars.v_empty[s]), C::TILES);
       mbar_init(smem_u32(&bars.s_full[s]), 1);
@@ -195,7 +200,6 @@ prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
   int issued = 0;    // the K/V copy warp: tiles whose copies it has issued
-  int q_loads = 0;   // the Q copy warp
 
   if (warp >= C::W_WIDE) {
     // ------------------------------------------------------------------ widening
@@ -208,24 +212,34 @@ prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
     auto widen = [&](uint32_t src, uint32_t dst, int valid, uint32_t lost) {
       constexpr int CH = D / 16;                            // 16-code chunks per row
       constexpr int ITER = C::N * CH / 128;
-#pragma unroll 4
-      for (int i = 0; i < ITER; ++i) {
-        const int unit = i * 16 + (ct >> 3);                // 8-row block x chunk
-        const int row = (unit / CH) * 8 + (ct & 7), ch = unit % CH;
-        uint32_t at;
-        if constexpr (D == 64) at = row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
-        else at = (ch >> 3) * C::N * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-        const uint4 u = lds128(src + at);
-        uint4 lo, hi;
-        lo.x = E4m3::to_f16x2(u.x); lo.y = E4m3::to_f16x2(u.x >> 16);
-        lo.z = E4m3::to_f16x2(u.y); lo.w = E4m3::to_f16x2(u.y >> 16);
-        hi.x = E4m3::to_f16x2(u.z); hi.y = E4m3::to_f16x2(u.z >> 16);
-        hi.z = E4m3::to_f16x2(u.w); hi.w = E4m3::to_f16x2(u.w >> 16);
-        if (row >= valid || ((lost >> (row >> 4)) & 1u)) lo = hi = make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t to = dst + (ch >> 2) * C::N * 128 + row * 128;
-        const int c = (ch & 3) * 2, x = row & 7;
-        st_shared_v4(to + ((c ^ x) << 4), lo);
-        st_shared_v4(to + (((c + 1) ^ x) << 4), hi);
+      constexpr int AT_ONCE = ITER < 8 ? ITER : 8;
+#pragma unroll 1
+      for (int i0 = 0; i0 < ITER; i0 += AT_ONCE) {
+        uint4 u[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+          const int unit = (i0 + i) * 16 + (ct >> 3);       // 8-row block x chunk
+          const int row = (unit / CH) * 8 + (ct & 7), ch = unit % CH;
+          uint32_t at;
+          if constexpr (D == 64) at = row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
+          else at = (ch >> 3) * C::N * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+          u[i] = lds128(src + at);
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+          const int unit = (i0 + i) * 16 + (ct >> 3);
+          const int row = (unit / CH) * 8 + (ct & 7), ch = unit % CH;
+          uint4 lo, hi;
+          lo.x = E4m3::to_f16x2(u[i].x); lo.y = E4m3::to_f16x2(u[i].x >> 16);
+          lo.z = E4m3::to_f16x2(u[i].y); lo.w = E4m3::to_f16x2(u[i].y >> 16);
+          hi.x = E4m3::to_f16x2(u[i].z); hi.y = E4m3::to_f16x2(u[i].z >> 16);
+          hi.z = E4m3::to_f16x2(u[i].w); hi.w = E4m3::to_f16x2(u[i].w >> 16);
+          if (row >= valid || ((lost >> (row >> 4)) & 1u)) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t to = dst + (ch >> 2) * C::N * 128 + row * 128;
+          const int c = (ch & 3) * 2, x = row & 7;
+          st_shared_v4(to + ((c ^ x) << 4), lo);
+          st_shared_v4(to + (((c + 1) ^ x) << 4), hi);
+        }
       }
     };
     bool ok = true;
@@ -236,96 +250,103 @@ prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
       if (!ok || it < 0) break;
       const WorkItem w = prm.items[it];
       const int nt = tiles_of(w);
-      float ref = 1.f;
-      // q rows to fp16 in place (each thread a row of each tile)
-      auto widen_q = [&] {
-        if (!mbar_wait_warp(smem_u32(&bars.q_raw), n & 1, limit, &abort_flag)) return false;
-        if constexpr (kWidenQ) {
-#pragma unroll 1
-          for (int i = 0; i < C::TILES; ++i) {
-            // (any order of a row's 16-byte pieces does; this one spreads the
-            // lanes over the banks)
-            const uint32_t row = base + C::OFF_Q + i * C::Q + ct * 128;
-            auto piece = [&](int c) {
-              return row + (c >> 3) * C::M * 128 + (((c ^ ct) & 7) << 4);
-            };
-            float a = 0.f;
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-              float f[8];
-              unpack8<E>(lds128(piece(c)), f);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float b = fabsf(f[e]);
-                a = b < INFINITY ? fmaxf(a, b) : a;
-              }
-            }
-            // q' = q 2^(13 - e) with 2^e <= a < 2^(e + 1)
-            const int e2 = max(int(__float_as_uint(a) >> 23) - 127, -100);
-            const float up = __uint_as_float(uint32_t(127 + min(13 - e2, 127)) << 23);
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-              const uint32_t at = piece(c);
-              float f[8];
-              unpack8<E>(lds128(at), f);
-              st_shared_v4(at, make_uint4(Fp16::pack2(f[0] * up, f[1] * up),
-                                          Fp16::pack2(f[2] * up, f[3] * up),
-                                          Fp16::pack2(f[4] * up, f[5] * up),
-                                          Fp16::pack2(f[6] * up, f[7] * up)));
-            }
-            // the score scale's exponent: e2 - 13 in -113..114
-            q_exp[n & 1][i * 128 + ct] = uint8_t(e2 - 13 + 128);
+      // ---- q as terms: D / 16 lanes per row, 16 elements each
+      if (n >= 1 && !mbar_wait_warp(smem_u32(&bars.q_empty), (n - 1) & 1, limit, &abort_flag)) {
+        ok = false;
+        break;
+      }
+      {
+        constexpr int LPR = D / 16, RPW = 32 / LPR;
+        const int q_end = prm.qo_indptr[w.req + 1];
+        const int ch = lane % LPR;
+#pragma unroll 2
+        for (int x = ct / LPR; x < C::TILES * C::M; x += 4 * RPW) {
+          const int i = x / C::M, row = x % C::M;
+          const int q_row = w.q_row + i * R + row / g;
+          uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+          if (q_row < q_end) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                reinterpret_cast<const uint16_t*>(q) +
+                (size_t(q_row) * prm.num_qo_heads + w.head * g + row % g) * D + ch * 16);
+            u[0] = src[0];
+            u[1] = src[1];
           }
-          fence_proxy_async_smem();
+          float f[16];
+          unpack8<E>(u[0], *reinterpret_cast<float(*)[8]>(f));
+          unpack8<E>(u[1], *reinterpret_cast<float(*)[8]>(f + 8));
+          float a = 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float b = fabsf(f[e]);
+            a = b < INFINITY ? fmaxf(a, b) : a;
+          }
+#pragma unroll
+          for (int d = LPR / 2; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+          // the smallest k >= -100 with a <= 448 * 2^k
+          const uint32_t au = __float_as_uint(a);
+          const int k = max(int(au >> 23) - 127 - 8 + ((au & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+          const float up = __uint_as_float(uint32_t(127 - k) << 23);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)   // (the conversion saturates infinities: NaN instead)
+            f[e] = fabsf(f[e]) < INFINITY ? f[e] * up : __uint_as_float(0x7fc00000u);
+          const int sw = C::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
+          const uint32_t dst = base + C::OFF_Q + i * C::Q + (ch >> 3) * C::M * 128 + row * C::ROWB +
+                               (((ch & 7) ^ sw) << 4);
+#pragma unroll
+          for (int tm = 0; tm < C::TERMS; ++tm) {
+            uint32_t code[4];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const uint32_t c = E4m3::from_f32x2(f[e], f[e + 1]);
+              const uint32_t h = E4m3::to_f16x2(c);
+              f[e] -= Fp16::lo(h);
+              f[e + 1] -= Fp16::hi(h);
+              if (e % 4 == 0) code[e / 4] = c;
+              else code[e / 4] |= c << 16;
+            }
+            st_shared_v4(dst + tm * C::QT, make_uint4(code[0], code[1], code[2], code[3]));
+          }
+          if (ch == 0) q_exp[n & 1][x] = uint8_t(k + 128);
         }
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
-        return true;
-      };
-      if (nt == 0) {
-        ok = widen_q();
-        continue;
       }
-      for (int j = 0; ok && j < nt; ++j) {
-        const int t = gt + j, rs = t % C::NRAW, rph = (t / C::NRAW) & 1, st = t & 1, ph = (t >> 1) & 1;
+      float ref = 1.f;
+      for (int j = 0; j < nt; ++j) {
+        const int t = gt + j, ks = t % C::NK, rs = t % C::NVR, st = t & 1;
         const int valid = min(C::N, w.tok_end - w.tok_begin - j * C::N);
-        // K: page scales, then the codes
-        ok = mbar_wait_warp(smem_u32(&bars.kr_full[rs]), rph, limit, &abort_flag) &&
-             (t < 2 || mbar_wait_warp(smem_u32(&bars.k_empty[st]), ph ^ 1, limit, &abort_flag));
-        if (!ok) break;
+        // the tile's page scales, which come with K
+        if (!mbar_wait_warp(smem_u32(&bars.k_full[ks]), (t / C::NK) & 1, limit, &abort_flag)) {
+          ok = false;
+          break;
+        }
         uint32_t lost = 0u;   // by 16 columns
         {
-          const int page = lane * 16 / P;
           const bool in = lane < C::NG && lane * 16 < valid;
-          const float2 s = in ? raw_scale[rs][page] : make_float2(1.f, 1.f);
+          const float2 s = in ? raw_scale[ks][lane * 16 / P] : make_float2(1.f, 1.f);
           const bool gone = in && s.x < 0.f;
           lost = __ballot_sync(0xffffffffu, gone);
           if (j == 0) ref = __shfl_sync(0xffffffffu, gone ? 1.f : s.y, 0);
-          if (ct < C::NG)     // the first warp writes them
-            scale_sh[t % kScaleRing][lane] =
-                make_float4(gone ? 0.f : s.x, gone ? 0.f : lg2(s.y),
-                            fminf(ref / s.y, 1.2676506e30f), ref);
-          if (ct == 0) lost_sh[t % kScaleRing] = int(lost);
-          if (ct < 32) {
+          if (ct < 32) {      // the first warp writes them
+            if (ct < C::NG)
+              scale_sh[t % kScaleRing][lane] =
+                  make_float4(gone ? 0.f : s.x, gone ? 0.f : lg2(s.y),
+                              fminf(ref / s.y, 1.2676506e30f), ref);
+            if (ct == 0) lost_sh[t % kScaleRing] = int(lost);
             __syncwarp();
             if (ct == 0) mbar_arrive(smem_u32(&bars.sc_full[t % kScaleRing]));
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.k_empty[ks]));
         }
-        widen(base + C::OFF_RAW + rs * C::RAW, base + C::OFF_K + st * C::KV, valid, lost);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&bars.kr_empty[rs]));
-          mbar_arrive(smem_u32(&bars.k_full[st]));
+        if (!mbar_wait_warp(smem_u32(&bars.vr_full[rs]), (t / C::NVR) & 1, limit, &abort_flag) ||
+            (t >= 2 && !mbar_wait_warp(smem_u32(&bars.v_empty[st]), ((t >> 1) & 1) ^ 1, limit,
+                                       &abort_flag))) {
+          ok = false;
+          break;
         }
-        if (j == 0) {
-          ok = widen_q();
-          if (!ok) break;
-        }
-        ok = mbar_wait_warp(smem_u32(&bars.vr_full[rs]), rph, limit, &abort_flag) &&
-             (t < 2 || mbar_wait_warp(smem_u32(&bars.v_empty[st]), ph ^ 1, limit, &abort_flag));
-        if (!ok) break;
-        widen(base + C::OFF_RAW + (C::NRAW + rs) * C::RAW, base + C::OFF_V + st * C::KV, valid, lost);
+        widen(base + C::OFF_VR + rs * C::CODES, base + C::OFF_V + st * C::V, valid, lost);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -344,7 +365,7 @@ prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
         prefetch_tensormap(&k_map);
         prefetch_tensormap(&v_map);
       }
-      const uint32_t box = uint32_t(P) * C::RAW_ROW;
+      const uint32_t box = uint32_t(P) * C::ROWB;
       auto publish = [&](int n, int value) {
         if (n >= kItemRing &&
             !mbar_wait_bounded(smem_u32(&bars.item_empty[n % kItemRing]),
@@ -390,7 +411,7 @@ prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
         if (nt == 0)
           next_page = more && lane < pages_in(wn, 0) ? prm.page_indices[wn.page_begin + lane] : -1;
         for (int j = 0; j < nt; ++j, ++t) {
-          const int rs = t % C::NRAW, rph = (t / C::NRAW) & 1;
+          const int ks = t % C::NK, rs = t % C::NVR;
           const int page = next_page;
           const bool mine = lane < pages_in(w, j);
           const bool valid = mine && page >= 0 && page < prm.num_pages;
@@ -403,37 +424,37 @@ prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
             next_page = prm.page_indices[wn.page_begin + lane];
           }
           const uint32_t bytes =
-              uint32_t(__popc(__ballot_sync(0xffffffffu, valid))) * C::RAW_BLK * box;
+              uint32_t(__popc(__ballot_sync(0xffffffffu, valid))) * C::BLK * box;
           const bool skip = t == 0 && prm.fault_kind == 1 && blockIdx.x == 0;
-          const uint32_t kf = smem_u32(&bars.kr_full[rs]), vf = smem_u32(&bars.vr_full[rs]);
-          if (t >= C::NRAW && !mbar_wait_warp(smem_u32(&bars.kr_empty[rs]), rph ^ 1, limit,
-                                              &abort_flag)) {
+          const uint32_t kf = smem_u32(&bars.k_full[ks]), vf = smem_u32(&bars.vr_full[rs]);
+          if (t >= C::NK && !mbar_wait_warp(smem_u32(&bars.k_empty[ks]), ((t / C::NK) & 1) ^ 1, limit,
+                                            &abort_flag)) {
             ok = false;
             break;
           }
           if (lane == 0 && !skip) mbar_arrive_expect_tx(kf, bytes);
           __syncwarp();
           if (valid && !skip) {
-            const uint32_t dst = base + C::OFF_RAW + rs * C::RAW + lane * box;
+            const uint32_t dst = base + C::OFF_K + ks * C::CODES + lane * box;
 #pragma unroll
-            for (int b = 0; b < C::RAW_BLK; ++b)
+            for (int b = 0; b < C::BLK; ++b)
               tma_load_4d(dst + b * C::N * 128, &k_map, kf, b * 128, c1, c2, page);
           }
           if (lane < ppt) {
             if (valid) {
               const size_t at = size_t(page) * hkv + w.head;
-              const uint32_t sc = smem_u32(&raw_scale[rs][lane]);
+              const uint32_t sc = smem_u32(&raw_scale[ks][lane]);
               cp_async4(sc, prm.k_head_scale + at);
               cp_async4(sc + 4, prm.v_head_scale + at);
               cp_async_arrive(kf);
             } else {
-              raw_scale[rs][lane] = make_float2(-1.f, 1.f);
+              raw_scale[ks][lane] = make_float2(-1.f, 1.f);
               mbar_arrive(kf);
             }
           }
           issued = t + 1;
-          if (t >= C::NRAW && !mbar_wait_warp(smem_u32(&bars.vr_empty[rs]), rph ^ 1, limit,
-                                              &abort_flag)) {
+          if (t >= C::NVR && !mbar_wait_warp(smem_u32(&bars.vr_empty[rs]), ((t / C::NVR) & 1) ^ 1,
+                                             limit, &abort_flag)) {
             ok = false;
             issued = -issued;   // K of this tile, not V
             break;
@@ -441,9 +462,9 @@ prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
           if (lane == 0) mbar_arrive_expect_tx(vf, bytes);
           __syncwarp();
           if (valid) {
-            const uint32_t dst = base + C::OFF_RAW + (C::NRAW + rs) * C::RAW + lane * box;
+            const uint32_t dst = base + C::OFF_VR + rs * C::CODES + lane * box;
 #pragma unroll
-            for (int b = 0; b < C::RAW_BLK; ++b)
+            for (int b = 0; b < C::BLK; ++b)
               tma_load_4d(dst + b * C::N * 128, &v_map, vf, b * 128, c1, c2, page);
           }
         }
@@ -453,36 +474,12 @@ prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
       if (!ok && lane == 0) fail();
       cp_async_wait_all();
       __syncwarp();
-    } else if (warp == C::W_Q) {
-      // ---------------------------------------------------------------- Q copies
-      bool ok = true;
-      for (int n = 0; ok; ++n) {
-        int it = -1;
-        ok = take_item(n, it);
-        if (!ok || it < 0) break;
-        const WorkItem w = prm.items[it];
-        if (n >= 1) ok = mbar_wait_warp(smem_u32(&bars.q_empty), (n - 1) & 1, limit, &abort_flag);
-        if (!ok) break;
-        if (lane == 0) {
-          const uint32_t qb = smem_u32(&bars.q_raw);
-          mbar_arrive_expect_tx(qb, C::TILES * C::Q);
-#pragma unroll
-          for (int i = 0; i < C::TILES; ++i)
-#pragma unroll
-            for (int c = 0; c < C::DBLK; ++c)
-              tma_load_3d(base + C::OFF_Q + i * C::Q + c * C::M * 128, &q_map, qb, c * 64,
-                          w.head * g, w.q_row + i * R);
-        }
-        q_loads = n + 1;
-      }
-      if (!ok && lane == 0) fail();
-      __syncwarp();
     } else if (warp < C::W_MMA + C::TILES) {
       // ------------------------------------------------------------- MMA issuers
       const int i = warp - C::W_MMA;
       if (lane == 0) {
-        const uint64_t qd0 = sdesc_sw128(base + C::OFF_Q + i * C::Q, 16, 1024);
-        const uint64_t kd0 = sdesc_sw128(base + C::OFF_K, 16, 1024);
+        const uint64_t qd0 = sdesc_swz(base + C::OFF_Q + i * C::Q, 16, C::ATOM, C::SWZ);
+        const uint64_t kd0 = sdesc_swz(base + C::OFF_K, 16, C::ATOM, C::SWZ);
         const uint64_t vd0 = sdesc_sw128(base + C::OFF_V, C::N * 128, 1024);
         const uint32_t s_col = tmem + C::col_s(i), o_col = tmem + C::col_o(i);
         auto wait = [&](uint64_t& bar, uint32_t parity) {
@@ -502,8 +499,8 @@ prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
           if (!active(w, i)) {
             // keeps the rings going: its share of each tile's release
             for (int j = 0; ok && j < nt; ++j, ++t) {
-              ok = wait(bars.k_full[t & 1], (t >> 1) & 1);
-              if (ok) mbar_arrive(smem_u32(&bars.k_empty[t & 1]));
+              ok = wait(bars.k_full[t % C::NK], (t / C::NK) & 1);
+              if (ok) mbar_arrive(smem_u32(&bars.k_empty[t % C::NK]));
               ok = ok && wait(bars.v_full[t & 1], (t >> 1) & 1);
               if (ok) mbar_arrive(smem_u32(&bars.v_empty[t & 1]));
             }
@@ -511,30 +508,33 @@ prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
             continue;
           }
           for (int j = 0; ok && j < nt; ++j, ++t, ++mine) {
-            const int st = t & 1, ph = (t >> 1) & 1;
+            const int st = t & 1, ph = (t >> 1) & 1, ks = t % C::NK;
             // (the K of later tiles was waited for while the previous tile's softmax ran)
-            if (j == 0) ok = wait(bars.k_full[st], ph);
+            if (j == 0) ok = wait(bars.k_full[ks], (t / C::NK) & 1);
             // S and P share columns, and the softmax rescales O after S is
             // full: the previous O += P V completes first
             if (ok && mine >= 1) ok = wait(bars.pv_done[i], (mine - 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t kd = kd0 + uint64_t((st * C::KV) >> 4);
+            const uint64_t kd = kd0 + uint64_t((ks * C::CODES) >> 4);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint64_t a = qd0 + uint64_t(((k >> 2) * C::M * 128 + (k & 3) * 32) >> 4);
-              const uint64_t b = kd + uint64_t(((k >> 2) * C::N * 128 + (k & 3) * 32) >> 4);
-              tc_mma_ss(s_col, a, b, C::IDESC_QK, k > 0 ? 1u : 0u);
-            }
+            for (int tm = 0; tm < C::TERMS; ++tm)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k) {
+                const int b = k * 32 / 128, o = k * 32 % 128;
+                tc_mma_f8_ss(s_col, qd0 + uint64_t((tm * C::QT + b * C::M * 128 + o) >> 4),
+                             kd + uint64_t((b * C::N * 128 + o) >> 4), C::IDESC_QK,
+                             (tm > 0 || k > 0) ? 1u : 0u);
+              }
             tc_commit(smem_u32(&bars.s_full[i]));
-            tc_commit(smem_u32(&bars.k_empty[st]));
+            tc_commit(smem_u32(&bars.k_empty[ks]));
             if (j == nt - 1) tc_commit(smem_u32(&bars.q_empty));
-            if (j + 1 < nt) ok = wait(bars.k_full[st ^ 1], ((t + 1) >> 1) & 1);
+            if (j + 1 < nt) ok = wait(bars.k_full[(t + 1) % C::NK], ((t + 1) / C::NK) & 1);
             if (ok) ok = wait(bars.v_full[st], ph);
             if (ok) ok = wait(bars.p_full[i], mine & 1);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t vd = vd0 + uint64_t((st * C::KV) >> 4);
+            const uint64_t vd = vd0 + uint64_t((st * C::V) >> 4);
 #pragma unroll
             for (int k = 0; k < C::N / 16; ++k)
               tc_mma_ts(o_col, s_col + k * 8, vd + uint64_t((k * 16 * 128) >> 4), C::IDESC_PV,
@@ -591,28 +591,24 @@ prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nt; ++j, ++gt, ++mine) {
         // The tiles' warpgroups take turns, so that one softmax runs while the
-        // tensor core works on the other tile.
-        bool turn = true;
-        if (both)
-          turn = i == 1 ? mbar_wait_warp(smem_u32(&bars.turn[0]), shared & 1, limit, &abort_flag)
-                        : (shared == 0 || mbar_wait_warp(smem_u32(&bars.turn[1]), (shared - 1) & 1,
-                                                         limit, &abort_flag));
-        if (!turn || !mbar_wait_warp(smem_u32(&bars.sc_full[gt % kScaleRing]),
-                                     (gt / kScaleRing) & 1, limit, &abort_flag) ||
-            !mbar_wait_warp(smem_u32(&bars.s_full[i]), mine & 1, limit, &abort_flag)) {
+        // tensor core works on the other tile. (The turn is waited for last: a
+        // wait costs two hundred cycles even where it is long over.)
+        if (!mbar_wait_warp(smem_u32(&bars.sc_full[gt % kScaleRing]), (gt / kScaleRing) & 1, limit,
+                            &abort_flag) ||
+            !mbar_wait_warp(smem_u32(&bars.s_full[i]), mine & 1, limit, &abort_flag) ||
+            (both && !(i == 1 ? mbar_wait_warp(smem_u32(&bars.turn[0]), shared & 1, limit, &abort_flag)
+                              : shared == 0 || mbar_wait_warp(smem_u32(&bars.turn[1]),
+                                                              (shared - 1) & 1, limit,
+                                                              &abort_flag)))) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (j == 0) {
-          // (the first scores are there, so the widened q and its exponents
-          // are. Waiting for q_full itself here would be wrong: where items
+          // (the first scores are there, so q's terms and exponents are. Waiting for q_full itself here would be wrong: where items
           // have one K tile, q_full runs on to the next item's phase while
           // this warp is still in the previous item's epilogue)
-          if constexpr (kWidenQ) {
-            const int e = int(q_exp[n & 1][i * 128 + t]) - 128;
-            unit *= __uint_as_float(uint32_t(127 + e) << 23);
-          }
+          unit *= __uint_as_float(uint32_t(int(q_exp[n & 1][i * 128 + t]) - 1) << 23);
           ref = scale_sh[gt % kScaleRing][0].w;
         }
         const int col0 = w.tok_begin + j * C::N;
@@ -769,22 +765,20 @@ prefill_page8_kernel(const __grid_constant__ CUtensorMap q_map,
   if (warp == C::W_KV && lane == 0) {
     const bool no_v = issued < 0;   // of the last tile
     if (no_v) issued = -issued;
-    for (int j = max(0, issued - C::NRAW); j < issued; ++j) {
+    for (int j = max(0, issued - C::NK); j < issued; ++j) {
       if (!(j == 0 && prm.fault_kind == 1 && blockIdx.x == 0))   // K never issued
-        mbar_wait_bounded(smem_u32(&bars.kr_full[j % C::NRAW]), (j / C::NRAW) & 1, limit, nullptr);
+        mbar_wait_bounded(smem_u32(&bars.k_full[j % C::NK]), (j / C::NK) & 1, limit, nullptr);
     }
     const int nv = no_v ? issued - 1 : issued;
-    for (int j = max(0, nv - C::NRAW); j < nv; ++j)
-      mbar_wait_bounded(smem_u32(&bars.vr_full[j % C::NRAW]), (j / C::NRAW) & 1, limit, nullptr);
+    for (int j = max(0, nv - C::NVR); j < nv; ++j)
+      mbar_wait_bounded(smem_u32(&bars.vr_full[j % C::NVR]), (j / C::NVR) & 1, limit, nullptr);
   }
-  if (warp == C::W_Q && lane == 0 && q_loads > 0)
-    mbar_wait_bounded(smem_u32(&bars.q_raw), (q_loads - 1) & 1, limit, nullptr);
 }
 
 template <int D, class E>
-cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
+cudaError_t launch_t(const void* q, const CUtensorMap& km, const CUtensorMap& vm,
                      const PrefillParams& p, int grid, cudaStream_t stream) {
-  using C = P8Cfg<D>;
+  using C = P8Cfg<D, E>;
   auto kern = prefill_page8_kernel<D, E>;
   static std::atomic<uint64_t> configured{0};
   const cudaError_t e = once_per_device(configured, [&] {
@@ -796,31 +790,31 @@ cudaError_t launch_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtenso
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (e != cudaSuccess) return e;
-  kern<<<grid, C::THREADS, C::SMEM, stream>>>(qm, km, vm, p);
+  kern<<<grid, C::THREADS, C::SMEM, stream>>>(q, km, vm, p);
   return cudaGetLastError();
 }
 
 template <class E>
-cudaError_t launch_d(int head_dim, const CUtensorMap& qm, const CUtensorMap& km,
+cudaError_t launch_d(int head_dim, const void* q, const CUtensorMap& km,
                      const CUtensorMap& vm, const PrefillParams& p, int grid, cudaStream_t stream) {
   switch (head_dim) {
-    case 64: return launch_t<64, E>(qm, km, vm, p, grid, stream);
-    case 128: return launch_t<128, E>(qm, km, vm, p, grid, stream);
-    case 256: return launch_t<256, E>(qm, km, vm, p, grid, stream);
+    case 64: return launch_t<64, E>(q, km, vm, p, grid, stream);
+    case 128: return launch_t<128, E>(q, km, vm, p, grid, stream);
+    case 256: return launch_t<256, E>(q, km, vm, p, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_prefill_page8(int head_dim, int dtype, const CUtensorMap& qm,
+cudaError_t launch_prefill_page8(int head_dim, int dtype, const void* q,
                                  const CUtensorMap& km, const CUtensorMap& vm,
                                  const PrefillParams& p, int num_sms, cudaStream_t stream) {
   const int grid = p.n_items < num_sms ? p.n_items : num_sms;
   if (grid <= 0) return cudaSuccess;
   switch (dtype) {
-    case FI_DTYPE_BF16: return launch_d<Bf16>(head_dim, qm, km, vm, p, grid, stream);
-    case FI_DTYPE_FP16: return launch_d<Fp16>(head_dim, qm, km, vm, p, grid, stream);
+    case FI_DTYPE_BF16: return launch_d<Bf16>(head_dim, q, km, vm, p, grid, stream);
+    case FI_DTYPE_FP16: return launch_d<Fp16>(head_dim, q, km, vm, p, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }
