@@ -88,6 +88,17 @@ struct E4m3 {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w & 0xffffu), __NV_E4M3);
     return uint32_t(h.x) | (uint32_t(h.y) << 16);
   }
+  // four packed e4m3 -> two fp16 pairs, first element low (exact)
+  __device__ static __forceinline__ uint2 to_f16x4(uint32_t w) {
+    uint2 r;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(r.x), "=r"(r.y)
+        : "r"(w));
+    return r;
+  }
   // two floats -> two packed e4m3 in the low 16 bits (a in the low byte),
   // rounded to nearest even, finite values saturated at +-448
   __device__ static __forceinline__ uint32_t from_f32x2(float a, float b) {

@@ -23,11 +23,13 @@
 // one exponential per score, and both sums keep their leading bits whatever
 // the spread of the scales.
 //
-// Roles (TILES = 2: 16 warps; TILES = 1: 12): a softmax warpgroup per tile
-// (thread = M row = TMEM lane; they take turns so that one tile's MMAs run
-// under the other's softmax), then the epilogue; a warp each to issue a tile's
-// MMAs and one to copy K/V pages and their scales; a warpgroup to turn q into
-// terms and widen V.
+// Roles (16 warps): 8 softmax warps, then the epilogue. They work on one M tile
+// after the other, two threads per row (TMEM lane), each on half of the keys:
+// while they are on one tile, the other's MMAs run. (A warpgroup per tile, a
+// thread per row, was slower: the warpgroups have to take turns for that
+// overlap, and one warp per scheduler waits for its own instructions.) A warp
+// each to issue a tile's MMAs and one to copy K/V pages and their scales; a
+// warpgroup to turn q into terms and widen V.
 #include <cfloat>
 #include <climits>
 #include <type_traits>
@@ -68,7 +70,7 @@ struct P8Cfg {
   static constexpr int V = N * D * 2;                       // one widened V tile
   static constexpr int QT = M * D;                          // one term of a tile's q
   static constexpr int Q = TERMS * QT;
-  static constexpr int NK = 3;                              // K tiles in flight
+  static constexpr int NK = TERMS == 3 && D >= 128 ? 2 : 3; // K tiles in flight
   static constexpr int NVR = TERMS == 3 && D >= 128 ? 1 : 2;   // V code tiles in flight
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + TILES * Q;
@@ -76,16 +78,14 @@ struct P8Cfg {
   static constexpr int OFF_VR = OFF_V + 2 * V;
   static constexpr int USED = OFF_VR + NVR * CODES;
   static constexpr int SMEM = (USED < 120 * 1024 ? 120 * 1024 : USED) + 1024;   // one CTA per SM
-  static_assert(SMEM <= 226 * 1024, "shared-memory budget");
-  static constexpr int SOFT = 4 * TILES;                    // softmax warps
+  static_assert(SMEM <= 220 * 1024, "shared-memory budget (and up to 6 KB of static arrays)");
+  static constexpr int SOFT = 8;                            // softmax warps: two threads per row
+  static constexpr int H = N / 2, HG = NG / 2;              // columns (16-column groups) per thread
   static constexpr int W_MMA = SOFT, W_KV = SOFT + 2, W_WIDE = SOFT + 4;
   static constexpr int THREADS = 32 * (SOFT + 8);
   // registers per thread at launch and, per warpgroup, after the split
-  static constexpr uint32_t LAUNCH_REGS = TILES == 2 ? 128 : 168;
-  static constexpr uint32_t SOFT_REGS = TILES == 2 ? 184 : 240;
-  static constexpr uint32_t HELP_REGS = TILES == 2 ? 56 : 104;
-  static constexpr uint32_t WIDE_REGS = TILES == 2 ? 88 : 160;
-  static_assert(TILES * SOFT_REGS + HELP_REGS + WIDE_REGS <= (TILES + 2) * LAUNCH_REGS, "");
+  static constexpr uint32_t LAUNCH_REGS = 128, SOFT_REGS = 160, HELP_REGS = 96, WIDE_REGS = 96;
+  static_assert(2 * SOFT_REGS + HELP_REGS + WIDE_REGS <= 4 * LAUNCH_REGS, "");
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t col_s(int i) { return uint32_t(i * N); }
   __host__ __device__ static constexpr uint32_t col_o(int i) { return uint32_t(TILES * N + i * D); }
@@ -101,7 +101,6 @@ struct P8Barriers {
   uint64_t v_full[2], v_empty[2];                              // widened tiles
   uint64_t s_full[2], p_full[2], pv_done[2], o_final[2], drain[2];
   uint64_t sc_full[kScaleRing];                                // a tile's page scales
-  uint64_t turn[2];                                            // the softmax warpgroups' turns
 };
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
@@ -124,6 +123,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
   __shared__ __align__(16) float4 scale_sh[kScaleRing][8];  // per 16 columns: s_k (-1: no page),
                                                             // log2 s_v, r / s_v, r
   __shared__ int lost_sh[kScaleRing];                       // the tile has a page outside the cache
+  __shared__ float pair_sh[2][2][128];                      // a row's halves: maxima, sums
   __shared__ uint8_t q_exp[2][C::TILES * 128];              // q rows' exponents + 128, by item parity
 
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -135,7 +135,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
   const int hkv = prm.num_qo_heads / g;
 
   auto item_at = [&](int n, int& idx) {
-    if (!mbar_wait_bounded(smem_u32(&bars.item_full[n % kItemRing]), (n / kItemRing) & 1, limit,
+    if (!mbar_sleep_bounded(smem_u32(&bars.item_full[n % kItemRing]), (n / kItemRing) & 1, limit,
                            &abort_flag))
       return false;
     idx = *reinterpret_cast<volatile int*>(&item_ring[n % kItemRing]);
@@ -181,11 +181,10 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
       mbar_init(smem_u32(&bars.v_full[s]), 4);
       mbar_init(smem_u32(&bars.v_empty[s]), C::TILES);
       mbar_init(smem_u32(&bars.s_full[s]), 1);
-      mbar_init(smem_u32(&bars.p_full[s]), 4);
+      mbar_init(smem_u32(&bars.p_full[s]), 8);
       mbar_init(smem_u32(&bars.pv_done[s]), 1);
       mbar_init(smem_u32(&bars.o_final[s]), 1);
       mbar_init(smem_u32(&bars.drain[s]), 1);
-      mbar_init(smem_u32(&bars.turn[s]), 4);
     }
     for (int s = 0; s < kScaleRing; ++s) mbar_init(smem_u32(&bars.sc_full[s]), 1);
     abort_flag = 0;
@@ -209,36 +208,37 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
     // of 64 dimensions). A warp's lanes take 8 rows x 4 chunks of 16 codes:
     // reads and writes then touch all banks evenly. Rows from `valid` on, and
     // those of pages outside the cache (bits of `lost`), become zero.
-    auto widen = [&](uint32_t src, uint32_t dst, int valid, uint32_t lost) {
-      constexpr int CH = D / 16;                            // 16-code chunks per row
-      constexpr int ITER = C::N * CH / 128;
+    // A thread keeps its chunk; its rows are 128 / CH apart, so that each address
+    // is the first one plus a constant.
+    constexpr int CH = D / 16;                              // 16-code chunks per row
+    constexpr int STEP = 128 / CH, ITER = C::N / STEP;
+    const int w_row = ((ct >> 3) / CH) * 8 + (ct & 7), w_ch = (ct >> 3) % CH;
+    const uint32_t w_src = base + C::OFF_VR + (w_ch >> 3) * C::N * 128 + w_row * C::ROWB +
+                           (((w_ch & 7) ^ (C::ROWB == 128 ? (w_row & 7) : ((w_row >> 1) & 3))) << 4);
+    const uint32_t w_dst = base + C::OFF_V + (w_ch >> 2) * C::N * 128 + w_row * 128;
+    const uint32_t w_lo = w_dst + ((((w_ch & 3) * 2) ^ (w_row & 7)) << 4);
+    const uint32_t w_hi = w_dst + ((((w_ch & 3) * 2 + 1) ^ (w_row & 7)) << 4);
+    auto widen = [&](int from, int to, int valid, uint32_t lost) {
+      const uint32_t src = w_src + from * C::CODES, lo = w_lo + to * C::V, hi = w_hi + to * C::V;
       constexpr int AT_ONCE = ITER < 8 ? ITER : 8;
-#pragma unroll 1
+#pragma unroll
       for (int i0 = 0; i0 < ITER; i0 += AT_ONCE) {
         uint4 u[AT_ONCE];
 #pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) {
-          const int unit = (i0 + i) * 16 + (ct >> 3);       // 8-row block x chunk
-          const int row = (unit / CH) * 8 + (ct & 7), ch = unit % CH;
-          uint32_t at;
-          if constexpr (D == 64) at = row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
-          else at = (ch >> 3) * C::N * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-          u[i] = lds128(src + at);
+        for (int i = 0; i < AT_ONCE; ++i) u[i] = lds128(src + (i0 + i) * STEP * C::ROWB);
+        if (valid < C::N || lost != 0u) {
+#pragma unroll
+          for (int i = 0; i < AT_ONCE; ++i) {
+            const int row = w_row + (i0 + i) * STEP;
+            if (row >= valid || ((lost >> (row >> 4)) & 1u)) u[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
-          const int unit = (i0 + i) * 16 + (ct >> 3);
-          const int row = (unit / CH) * 8 + (ct & 7), ch = unit % CH;
-          uint4 lo, hi;
-          lo.x = E4m3::to_f16x2(u[i].x); lo.y = E4m3::to_f16x2(u[i].x >> 16);
-          lo.z = E4m3::to_f16x2(u[i].y); lo.w = E4m3::to_f16x2(u[i].y >> 16);
-          hi.x = E4m3::to_f16x2(u[i].z); hi.y = E4m3::to_f16x2(u[i].z >> 16);
-          hi.z = E4m3::to_f16x2(u[i].w); hi.w = E4m3::to_f16x2(u[i].w >> 16);
-          if (row >= valid || ((lost >> (row >> 4)) & 1u)) lo = hi = make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t to = dst + (ch >> 2) * C::N * 128 + row * 128;
-          const int c = (ch & 3) * 2, x = row & 7;
-          st_shared_v4(to + ((c ^ x) << 4), lo);
-          st_shared_v4(to + (((c + 1) ^ x) << 4), hi);
+          const uint2 a = E4m3::to_f16x4(u[i].x), b = E4m3::to_f16x4(u[i].y);
+          const uint2 c = E4m3::to_f16x4(u[i].z), d = E4m3::to_f16x4(u[i].w);
+          st_shared_v4(lo + (i0 + i) * STEP * 128, make_uint4(a.x, a.y, b.x, b.y));
+          st_shared_v4(hi + (i0 + i) * STEP * 128, make_uint4(c.x, c.y, d.x, d.y));
         }
       }
     };
@@ -251,7 +251,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
       const WorkItem w = prm.items[it];
       const int nt = tiles_of(w);
       // ---- q as terms: D / 16 lanes per row, 16 elements each
-      if (n >= 1 && !mbar_wait_warp(smem_u32(&bars.q_empty), (n - 1) & 1, limit, &abort_flag)) {
+      if (n >= 1 && !mbar_sleep_warp(smem_u32(&bars.q_empty), (n - 1) & 1, limit, &abort_flag)) {
         ok = false;
         break;
       }
@@ -317,7 +317,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
         const int t = gt + j, ks = t % C::NK, rs = t % C::NVR, st = t & 1;
         const int valid = min(C::N, w.tok_end - w.tok_begin - j * C::N);
         // the tile's page scales, which come with K
-        if (!mbar_wait_warp(smem_u32(&bars.k_full[ks]), (t / C::NK) & 1, limit, &abort_flag)) {
+        if (!mbar_sleep_warp(smem_u32(&bars.k_full[ks]), (t / C::NK) & 1, limit, &abort_flag)) {
           ok = false;
           break;
         }
@@ -340,13 +340,13 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars.k_empty[ks]));
         }
-        if (!mbar_wait_warp(smem_u32(&bars.vr_full[rs]), (t / C::NVR) & 1, limit, &abort_flag) ||
-            (t >= 2 && !mbar_wait_warp(smem_u32(&bars.v_empty[st]), ((t >> 1) & 1) ^ 1, limit,
+        if (!mbar_sleep_warp(smem_u32(&bars.vr_full[rs]), (t / C::NVR) & 1, limit, &abort_flag) ||
+            (t >= 2 && !mbar_sleep_warp(smem_u32(&bars.v_empty[st]), ((t >> 1) & 1) ^ 1, limit,
                                        &abort_flag))) {
           ok = false;
           break;
         }
-        widen(base + C::OFF_VR + rs * C::CODES, base + C::OFF_V + st * C::V, valid, lost);
+        widen(rs, st, valid, lost);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -368,7 +368,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
       const uint32_t box = uint32_t(P) * C::ROWB;
       auto publish = [&](int n, int value) {
         if (n >= kItemRing &&
-            !mbar_wait_bounded(smem_u32(&bars.item_empty[n % kItemRing]),
+            !mbar_sleep_bounded(smem_u32(&bars.item_empty[n % kItemRing]),
                                ((n / kItemRing) & 1) ^ 1, limit, &abort_flag))
           return false;
         item_ring[n % kItemRing] = value;
@@ -427,7 +427,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
               uint32_t(__popc(__ballot_sync(0xffffffffu, valid))) * C::BLK * box;
           const bool skip = t == 0 && prm.fault_kind == 1 && blockIdx.x == 0;
           const uint32_t kf = smem_u32(&bars.k_full[ks]), vf = smem_u32(&bars.vr_full[rs]);
-          if (t >= C::NK && !mbar_wait_warp(smem_u32(&bars.k_empty[ks]), ((t / C::NK) & 1) ^ 1, limit,
+          if (t >= C::NK && !mbar_sleep_warp(smem_u32(&bars.k_empty[ks]), ((t / C::NK) & 1) ^ 1, limit,
                                             &abort_flag)) {
             ok = false;
             break;
@@ -453,7 +453,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
             }
           }
           issued = t + 1;
-          if (t >= C::NVR && !mbar_wait_warp(smem_u32(&bars.vr_empty[rs]), ((t / C::NVR) & 1) ^ 1,
+          if (t >= C::NVR && !mbar_sleep_warp(smem_u32(&bars.vr_empty[rs]), ((t / C::NVR) & 1) ^ 1,
                                              limit, &abort_flag)) {
             ok = false;
             issued = -issued;   // K of this tile, not V
@@ -483,7 +483,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
         const uint64_t vd0 = sdesc_sw128(base + C::OFF_V, C::N * 128, 1024);
         const uint32_t s_col = tmem + C::col_s(i), o_col = tmem + C::col_o(i);
         auto wait = [&](uint64_t& bar, uint32_t parity) {
-          return mbar_wait_bounded(smem_u32(&bar), parity, limit, &abort_flag);
+          return mbar_sleep_bounded(smem_u32(&bar), parity, limit, &abort_flag);
         };
         bool ok = true;
         int t = 0;      // tiles of earlier items
@@ -549,207 +549,242 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
         if (!ok) fail();
         // every MMA issued so far completes before the TMEM is released
         tc_commit(smem_u32(&bars.drain[i]));
-        mbar_wait_bounded(smem_u32(&bars.drain[i]), 0, limit, nullptr);
+        mbar_sleep_bounded(smem_u32(&bars.drain[i]), 0, limit, nullptr);
       }
       __syncwarp();
     }
   } else {
     setmaxnreg_inc<C::SOFT_REGS>();
     // ------------------------------------------------------- softmax + epilogue
-    const int i = warp >> 2;
-    const int t = (warp & 3) * 32 + lane;             // M row of the tile = TMEM lane
-    const int row_in = i * R + t / g;                 // query row within the item
+    const int half = warp >> 2;                       // which half of a row's columns
+    const int t = (warp & 3) * 32 + lane;             // M row of a tile = TMEM lane
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t s_col = tmem + lane_off + C::col_s(i);
-    const uint32_t o_col = tmem + lane_off + C::col_o(i);
     const float scale0 = prm.sm_scale * kLog2e;
+    // The two warps of 32 rows meet at a named barrier, so neither leaves an
+    // item alone: after a wait that ran out (`ok` false; no wait waits any more)
+    // a warp goes through the rest of its item, and the vote at the next item's
+    // start ends both.
+    const int pair_bar = 1 + (warp & 3);
     bool ok = true;
-    int gt = 0;      // tiles of earlier items
-    int mine = 0;    // of which this tile took part in
-    int shared = 0;  // and of which both did
-    int outs = 0;    // items with keys this tile took part in
-    for (int n = 0; ok; ++n) {
+    auto wait = [&](uint64_t& bar, uint32_t parity) {
+      if (ok && !mbar_sleep_warp(smem_u32(&bar), parity, limit, &abort_flag)) {
+        ok = false;
+        abort_flag = 1;
+      }
+    };
+    // A value of the row's other half (two buffers in turn: the next value may
+    // be written while the other warp still reads this one).
+    int swaps = 0;
+    auto swap = [&](float mine) {
+      float(*buf)[128] = pair_sh[swaps++ & 1];
+      buf[half][t] = mine;
+      tc_fence_before();
+      named_bar_sync(pair_bar, 64);
+      tc_fence_after();
+      return buf[half ^ 1][t];
+    };
+    int gt = 0;                    // tiles of keys of earlier items
+    int done0 = 0, done1 = 0;      // of which each M tile took part in
+    int outs0 = 0, outs1 = 0;      // items with keys each M tile took part in
+    for (int n = 0;; ++n) {
       int it = -1;
-      ok = take_item(n, it);
+      if (ok) ok = take_item(n, it);
+      ok = !named_bar_or(pair_bar, 64, !ok);
       if (!ok || it < 0) break;
       const WorkItem w = prm.items[it];
       const int nt = tiles_of(w);
-      const bool both = C::TILES == 2 && active(w, 1);
-      if (i == 1 && !both) {
-        gt += nt;
-        continue;
-      }
       const int q_start = prm.qo_indptr[w.req], q_end = prm.qo_indptr[w.req + 1];
       const int np_req = prm.page_indptr[w.req + 1] - prm.page_indptr[w.req];
       const int kv_len = np_req > 0 ? (np_req - 1) * P + prm.last_page_len[w.req] : 0;
-      const int q_row = w.q_row + row_in;
-      const int pos = kv_len - (q_end - q_start) + (q_row - q_start);   // key position
-      const int t_max = min(prm.causal ? pos : kv_len - 1, kv_len - 1);
-      const int t_min = prm.window_left >= 0 ? pos - prm.window_left : INT_MIN;
-      float unit = scale0;   // the row's score scale (the page's s_k joins it)
-      float ref = 1.f;       // r
-      float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < nt; ++j, ++gt, ++mine) {
-        // The tiles' warpgroups take turns, so that one softmax runs while the
-        // tensor core works on the other tile. (The turn is waited for last: a
-        // wait costs two hundred cycles even where it is long over.)
-        if (!mbar_wait_warp(smem_u32(&bars.sc_full[gt % kScaleRing]), (gt / kScaleRing) & 1, limit,
-                            &abort_flag) ||
-            !mbar_wait_warp(smem_u32(&bars.s_full[i]), mine & 1, limit, &abort_flag) ||
-            (both && !(i == 1 ? mbar_wait_warp(smem_u32(&bars.turn[0]), shared & 1, limit, &abort_flag)
-                              : shared == 0 || mbar_wait_warp(smem_u32(&bars.turn[1]),
-                                                              (shared - 1) & 1, limit,
-                                                              &abort_flag)))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (j == 0) {
-          // (the first scores are there, so q's terms and exponents are. Waiting for q_full itself here would be wrong: where items
-          // have one K tile, q_full runs on to the next item's phase while
-          // this warp is still in the previous item's epilogue)
-          unit *= __uint_as_float(uint32_t(int(q_exp[n & 1][i * 128 + t]) - 1) << 23);
-          ref = scale_sh[gt % kScaleRing][0].w;
-        }
-        const int col0 = w.tok_begin + j * C::N;
-        const int hi = t_max - col0;
-        const int lo = t_min > col0 ? t_min - col0 : 0;
-        const uint32_t lost = uint32_t(lost_sh[gt % kScaleRing]);
-        const float4* sc = scale_sh[gt % kScaleRing];
-        const bool need_mask = __any_sync(0xffffffffu, hi < C::N - 1 || lo > 0) || lost != 0u;
-        auto body = [&](auto masked) {
-          constexpr bool MK = decltype(masked)::value;
-          uint32_t sr[C::N / 32][32];
-#pragma unroll
-          for (int c = 0; c < C::N / 32; ++c) tmem_ld32(s_col + c * 32, sr[c]);
-          tmem_wait_ld();
-          if (MK) {
-#pragma unroll
-            for (int k = 0; k < C::N; ++k)
-              if (k > hi || k < lo || ((lost >> (k >> 4)) & 1u)) sr[k >> 5][k & 31] = 0xff800000u;
-          }
-          // s + log2 s_v of a group's largest score; the scale is at least
-          // FLT_MIN (a hidden score is -inf, and -inf * 0 would be NaN)
-          float cu[C::NG], lv[C::NG];
-          float m_tile = -INFINITY;
-#pragma unroll
-          for (int p = 0; p < C::NG; ++p) {
-            const float2 s = *reinterpret_cast<const float2*>(sc + p);
-            cu[p] = fmaxf(s.x * unit, FLT_MIN);
-            lv[p] = s.y;
-            float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const int k = p * 16 + e;
-              a = fmax3(a, __uint_as_float(sr[k >> 5][k & 31]),
-                        __uint_as_float(sr[k >> 5][(k + 1) & 31]));
-              b = fmax3(b, __uint_as_float(sr[k >> 5][(k + 2) & 31]),
-                        __uint_as_float(sr[k >> 5][(k + 3) & 31]));
-            }
-            m_tile = fmaxf(m_tile, fmaf(fmaxf(a, b), cu[p], lv[p]));
-          }
-          const float m_new = fmaxf(m, m_tile);
-          const bool grow = m_new > m + kRescaleThreshold;
-          const bool o_live = grow && m != -INFINITY;
-          float alpha = 1.f;
-          if (grow) {
-            alpha = ex2(m - m_new);
-            l *= alpha;
-            m = m_new;
-          }
-          // O is settled: this S was issued after the previous O += P V had completed
-          if (__any_sync(0xffffffffu, o_live)) {
+      const int n_act = w.q_row + R < q_end ? C::TILES : 1;             // M tiles with a row
+      // key position of this thread's row of tile 0 (tile 1: R rows on), and
+      // the keys it may see, in columns of this thread's half
+      const int row0 = w.q_row + t / g;
+      const int pos0 = kv_len - (q_end - q_start) + (row0 - q_start);
+      const int off = w.tok_begin + half * C::H;
+      // tiles of keys that cross a bound of some row of this warp: from `last`
+      // on, and with a window before `first` (a row past the request's last one
+      // counts as the last one)
+      const int col_row = prm.causal ? pos0 : kv_len - 1;
+      const int low = __reduce_min_sync(0xffffffffu, min(col_row, kv_len - 1));
+      const int high = __reduce_max_sync(0xffffffffu, pos0) + (C::TILES - 1) * R;
+      const int last = low - off < C::H - 1 ? 0 : (low - off - (C::H - 1)) / C::N + 1;
+      const int first = prm.window_left >= 0 ? (high - prm.window_left - off + C::N - 1) / C::N : 0;
+      float unit0 = 0.f, unit1 = 0.f, m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+      float ref = 1.f;             // r
+      for (int j = 0; j < nt; ++j, ++gt) {
+        wait(bars.sc_full[gt % kScaleRing], (gt / kScaleRing) & 1);
+        const uint32_t lost = uint32_t(lost_sh[gt % kScaleRing]) >> (half * C::HG);
+        const float4* sc = scale_sh[gt % kScaleRing] + half * C::HG;
+        // (one copy of this code, for the instruction cache: unrolled over the
+        // M tiles, or with a second copy for masked tiles, it was slower)
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t r[16];
-              tmem_ld16(o_col + c * 16, r);
-              tmem_wait_ld();
+        for (int i = 0; i < n_act; ++i) {
+          wait(bars.s_full[i], (i == 0 ? done0++ : done1++) & 1);
+          tc_fence_after();
+          float unit = i == 0 ? unit0 : unit1;
+          float m = i == 0 ? m0 : m1, l = i == 0 ? l0 : l1;
+          if (j == 0) {
+            // (the first scores are there, so q's terms and exponents are.
+            // Waiting for q_full itself here would be wrong: where items have
+            // one tile of keys, q_full runs on to the next item's phase while
+            // this warp is still in the previous item's epilogue)
+            unit = scale0 * __uint_as_float(uint32_t(int(q_exp[n & 1][i * 128 + t]) - 1) << 23);
+            if (i == 0) unit0 = unit;
+            else unit1 = unit;
+            if (i == 0) ref = scale_sh[gt % kScaleRing][0].w;
+          }
+          const uint32_t s_col = tmem + lane_off + C::col_s(i);
+          const uint32_t o_col = tmem + lane_off + C::col_o(i) + half * (D / 2);
+          const bool need_mask = j >= last || j < first || lost != 0u;
+          {
+            uint32_t sr[C::H / 32][32];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-              tmem_st16(o_col + c * 16, r);
+            for (int c = 0; c < C::H / 32; ++c) tmem_ld32(s_col + half * C::H + c * 32, sr[c]);
+            tmem_wait_ld();
+            if (need_mask) {
+              const int pos = pos0 + i * R, col0 = off + j * C::N;
+              const int hi = min(prm.causal ? pos : kv_len - 1, kv_len - 1) - col0;
+              const int lo = prm.window_left >= 0 ? max(pos - prm.window_left - col0, 0) : 0;
+#pragma unroll
+              for (int k = 0; k < C::H; ++k)
+                if (k > hi || k < lo || ((lost >> (k >> 4)) & 1u)) sr[k >> 5][k & 31] = 0xff800000u;
+            }
+            // s + log2 s_v of a group's largest score; the scale is at least
+            // FLT_MIN (a hidden score is -inf, and -inf * 0 would be NaN)
+            float cu[C::HG], lv[C::HG];
+            float m_tile = -INFINITY;
+#pragma unroll
+            for (int p = 0; p < C::HG; ++p) {
+              const float2 s = *reinterpret_cast<const float2*>(sc + p);
+              cu[p] = fmaxf(s.x * unit, FLT_MIN);
+              lv[p] = s.y;
+              float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const int k = p * 16 + e;
+                a = fmax3(a, __uint_as_float(sr[k >> 5][k & 31]),
+                          __uint_as_float(sr[k >> 5][(k + 1) & 31]));
+                b = fmax3(b, __uint_as_float(sr[k >> 5][(k + 2) & 31]),
+                          __uint_as_float(sr[k >> 5][(k + 3) & 31]));
+              }
+              m_tile = fmaxf(m_tile, fmaf(fmaxf(a, b), cu[p], lv[p]));
+            }
+            const float m_other = swap(m_tile);
+            const float m_new = fmax3(m, m_tile, m_other);
+            const bool grow = m_new > m + kRescaleThreshold;
+            const bool o_live = grow && m != -INFINITY;
+            float alpha = 1.f;
+            if (grow) {
+              alpha = ex2(m - m_new);
+              l *= alpha;
+              m = m_new;
+            }
+            // O is settled: this S was issued after the previous O += P V had
+            // completed. Each warp rescales half of the columns.
+            if (__any_sync(0xffffffffu, o_live)) {
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t r[16];
+                tmem_ld16(o_col + c * 16, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                tmem_st16(o_col + c * 16, r);
+              }
+              tmem_wait_st();
+            }
+            const float mm = m == -INFINITY ? 0.f : m;
+            // P over S's first columns: both halves of S were read before the
+            // barrier above
+#pragma unroll
+            for (int p = 0; p < C::HG; p += 2) {
+              uint32_t wv[16];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float b = lv[p + h] - mm;
+                const float2 c2 = make_float2(cu[p + h], cu[p + h]), b2 = make_float2(b, b);
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                  const int k = (p + h) * 16 + e;
+                  const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[k >> 5][k & 31]),
+                                                          __uint_as_float(sr[k >> 5][(k + 1) & 31])),
+                                              c2, b2);
+                  const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                  sum = __fadd2_rn(sum, y);
+                  wv[h * 8 + e / 2] = Fp16::pack2(y.x, y.y);
+                }
+                l = fmaf(sum.x + sum.y, sc[p + h].z, l);
+              }
+              tmem_st16(s_col + half * (C::H / 2) + p * 8, wv);
             }
             tmem_wait_st();
           }
-          const float mm = m == -INFINITY ? 0.f : m;
-#pragma unroll
-          for (int p = 0; p < C::NG; p += 2) {
-            uint32_t wv[16];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float b = lv[p + h] - mm;
-              const float2 c2 = make_float2(cu[p + h], cu[p + h]), b2 = make_float2(b, b);
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const int k = (p + h) * 16 + e;
-                const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[k >> 5][k & 31]),
-                                                        __uint_as_float(sr[k >> 5][(k + 1) & 31])),
-                                            c2, b2);
-                const float2 y = make_float2(ex2(x.x), ex2(x.y));
-                sum = __fadd2_rn(sum, y);
-                wv[h * 8 + e / 2] = Fp16::pack2(y.x, y.y);
-              }
-              l = fmaf(sum.x + sum.y, sc[p + h].z, l);
-            }
-            tmem_st16(s_col + p * 8, wv);
+          if (i == 0) {
+            m0 = m;
+            l0 = l;
+          } else {
+            m1 = m;
+            l1 = l;
           }
-          tmem_wait_st();
-        };
-        if (need_mask) body(std::true_type{});
-        else body(std::false_type{});
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&bars.p_full[i]));
-          if (both) mbar_arrive(smem_u32(&bars.turn[i]));
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[i]));
         }
-        shared += both ? 1 : 0;
       }
-      if (!ok) break;
-      if (nt > 0) {
-        if (!mbar_wait_warp(smem_u32(&bars.o_final[i]), outs & 1, limit, &abort_flag)) {
-          ok = false;
-          break;
-        }
-        ++outs;
-      }
-      tc_fence_after();
-      // ---- epilogue (a piece of a split item writes the rows' fp32 states)
-      const bool row_ok = q_row < q_end;
-      const float inv = l == 0.f ? 0.f : prm.v_scale * ref / l;
-      const int head = w.head * g + t % g;
-      const bool piece = w.merge > 0;
-      const size_t orow = piece ? size_t(w.slot) + size_t(row_in) * size_t(w.merge) : size_t(q_row);
-      const size_t at = orow * prm.num_qo_heads + head;
+      // ---- epilogue, half of the columns per warp (a piece of a split item
+      // writes the rows' fp32 states)
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t r[32];
-        if (nt > 0) {
-          tmem_ld32(o_col + c * 32, r);
-          tmem_wait_ld();
-        } else {
+      for (int i = 0; i < n_act; ++i) {
+        if (nt > 0) wait(bars.o_final[i], (i == 0 ? outs0++ : outs1++) & 1);
+        const float m = i == 0 ? m0 : m1, l = i == 0 ? l0 : l1;
+        const float l_other = swap(l);
+        const float sum = half == 0 ? l + l_other : l_other + l;
+        const uint32_t o_col = tmem + lane_off + C::col_o(i) + half * (D / 2);
+        const int row_in = i * R + t / g;               // query row within the item
+        const int q_row = w.q_row + row_in;
+        const bool row_ok = q_row < q_end;
+        const float inv = sum == 0.f ? 0.f : prm.v_scale * ref / sum;
+        const int head = w.head * g + t % g;
+        const bool piece = w.merge > 0;
+        const size_t orow =
+            piece ? size_t(w.slot) + size_t(row_in) * size_t(w.merge) : size_t(q_row);
+        const size_t at = orow * prm.num_qo_heads + head;
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t r[32];
+          if (nt > 0) {
+            tmem_ld32(o_col + c * 32, r);
+            tmem_wait_ld();
+          } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = 0u;
-        }
-        const float* f = reinterpret_cast<const float*>(r);
-        if (row_ok && piece) {
-          float4* dst = reinterpret_cast<float4*>(prm.piece_o + at * D + c * 32);
+            for (int e = 0; e < 32; ++e) r[e] = 0u;
+          }
+          const float* f = reinterpret_cast<const float*>(r);
+          const size_t to = at * D + half * (D / 2) + c * 32;
+          if (row_ok && piece) {
+            float4* dst = reinterpret_cast<float4*>(prm.piece_o + to);
 #pragma unroll
-          for (int q4 = 0; q4 < 8; ++q4)
-            dst[q4] = make_float4(f[q4 * 4] * inv, f[q4 * 4 + 1] * inv, f[q4 * 4 + 2] * inv,
-                                  f[q4 * 4 + 3] * inv);
-        } else if (row_ok) {
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(prm.out) + at * D + c * 32);
+            for (int q4 = 0; q4 < 8; ++q4)
+              dst[q4] = make_float4(f[q4 * 4] * inv, f[q4 * 4 + 1] * inv, f[q4 * 4 + 2] * inv,
+                                    f[q4 * 4 + 3] * inv);
+          } else if (row_ok) {
+            uint4* dst =
+                reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(prm.out) + to);
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            const float* x = f + q4 * 8;
-            dst[q4] = make_uint4(E::pack2(x[0] * inv, x[1] * inv), E::pack2(x[2] * inv, x[3] * inv),
-                                 E::pack2(x[4] * inv, x[5] * inv), E::pack2(x[6] * inv, x[7] * inv));
+            for (int q4 = 0; q4 < 4; ++q4) {
+              const float* x = f + q4 * 8;
+              dst[q4] =
+                  make_uint4(E::pack2(x[0] * inv, x[1] * inv), E::pack2(x[2] * inv, x[3] * inv),
+                             E::pack2(x[4] * inv, x[5] * inv), E::pack2(x[6] * inv, x[7] * inv));
+            }
           }
         }
+        float* lse = piece ? prm.piece_lse : prm.lse;
+        if (half == 0 && row_ok && lse)
+          lse[at] = sum == 0.f ? -INFINITY : (m + (lg2(sum) - lg2(ref))) * kLn2;
       }
-      float* lse = piece ? prm.piece_lse : prm.lse;
-      if (row_ok && lse) lse[at] = l == 0.f ? -INFINITY : (m + (lg2(l) - lg2(ref))) * kLn2;
       tc_fence_before();
     }
     if (!ok && lane == 0) fail();
@@ -767,11 +802,11 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
     if (no_v) issued = -issued;
     for (int j = max(0, issued - C::NK); j < issued; ++j) {
       if (!(j == 0 && prm.fault_kind == 1 && blockIdx.x == 0))   // K never issued
-        mbar_wait_bounded(smem_u32(&bars.k_full[j % C::NK]), (j / C::NK) & 1, limit, nullptr);
+        mbar_sleep_bounded(smem_u32(&bars.k_full[j % C::NK]), (j / C::NK) & 1, limit, nullptr);
     }
     const int nv = no_v ? issued - 1 : issued;
     for (int j = max(0, nv - C::NVR); j < nv; ++j)
-      mbar_wait_bounded(smem_u32(&bars.vr_full[j % C::NVR]), (j / C::NVR) & 1, limit, nullptr);
+      mbar_sleep_bounded(smem_u32(&bars.vr_full[j % C::NVR]), (j / C::NVR) & 1, limit, nullptr);
   }
 }
 

@@ -71,6 +71,32 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same wait with a suspend-time hint of 20 us: the thread sleeps until the
+// phase completes instead of polling, which leaves the issue slots to the
+// warps beside it. The abort flag and the limit are looked at between sleeps.
+__device__ __forceinline__ bool mbar_sleep_bounded(uint32_t bar, uint32_t parity,
+                                                   uint64_t limit_ns,
+                                                   const volatile int* abort) {
+  auto attempt = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+  };
+  if (attempt()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (attempt()) return true;
+    if (abort && *abort) return false;
+    if (globaltimer_ns() - t0 > limit_ns) return false;
+  }
+}
+
 // ---- TMA (tensor-map) loads into shared memory, completion on an mbarrier
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int c0, int c1, int c2) {
@@ -105,6 +131,12 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                                const volatile int* abort) {
   const bool ok = mbar_wait_bounded(bar, parity, limit_ns, abort);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ bool mbar_sleep_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                                const volatile int* abort) {
+  const bool ok = mbar_sleep_bounded(bar, parity, limit_ns, abort);
   return __all_sync(0xffffffffu, ok);
 }
 
