@@ -19,16 +19,21 @@
 // is at least 16 for M = 128, so up to 8 heads x 2 terms cost nothing extra.
 //
 // Scales: the score of a key is multiplied by its page's s_k with the softmax
-// scale. A weight is multiplied by its page's s_v before it is rounded, p s_v
-// = 2^(s + log2 s_v), with a running maximum of its own: sums of p (the
-// denominator and lse) and of p s_v v then both keep their leading bits, for
-// any spread of the pages' scales.
+// scale. The page's s_v joins the weight before it is rounded:
+//   w = 2^(s + log2 s_v - m),  m the running maximum of s + log2 s_v,
+//   O = sum w code,  l = sum w r / s_v (r: s_v of the item's first page),
+//   out = O r / l,   lse = ln 2 (m + log2 l - log2 r):
+// one exponential per score, and both sums keep their leading bits whatever
+// the spread of the scales.
 //
-// Roles (6 warps): 0-3 softmax (thread = key of the tile = TMEM lane), then
+// Roles (7 warps): 0-3 softmax (thread = key of the tile = TMEM lane), then
 // the epilogue (thread = dimension); 4 copies pages by TMA and page scales by
 // cp.async into a ring; 5 issues the MMAs (the scores of tile j + 1 before the
-// output of tile j, with two score buffers). The launch is persistent: a CTA
-// takes items from a counter and the ring runs on from item to item.
+// output of tile j, with two score buffers); 6 merges the states of requests
+// whose last chunk this CTA finished, beside the next items. The launch is
+// persistent: a CTA takes items from a counter, the ring runs on from item to
+// item, and an item's q is loaded and turned into terms before the previous
+// item's epilogue (an item's start and end had cost as much as four tiles).
 #include <cfloat>
 #include <type_traits>
 
@@ -71,11 +76,12 @@ struct D8Cfg {
   static constexpr int OFF_Q = NST * STAGE;                 // two buffers
   static constexpr int OFF_P = OFF_Q + 2 * QBYTES;          // two buffers
   static constexpr int SMEM = OFF_P + 2 * PBYTES + 1024;
-  static constexpr int THREADS = 192;
+  static constexpr int THREADS = 224;
   static constexpr uint32_t TMEM_COLS = N * (2 + DB) <= 64 ? 64 : 128;
   static constexpr uint32_t IDESC_S = idesc_e4m3(128, N, 0, 0);
   static constexpr uint32_t IDESC_O = idesc_e4m3(128, 16, 1, 1);
   static constexpr int DPL = D / 32;                        // q elements per lane and head
+  static constexpr int HPW = (G + 3) / 4;                   // heads whose q a softmax warp loads
   static_assert(SMEM * CTAS <= 227 * 1024, "shared-memory budget");
   static_assert(COLS <= 32 && N * (2 + DB) <= 128, "");
 };
@@ -84,6 +90,7 @@ struct D8Barriers {
   uint64_t item_full[kItemRing], item_empty[kItemRing];
   uint64_t k_full[6], v_full[6], empty[6];
   uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t m_full[2], m_empty[2];   // finished chunks for the merging warp
   uint64_t drain;
 };
 
@@ -113,8 +120,8 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
   __shared__ int item_ring[kItemRing];
   __shared__ __align__(8) float2 scale_sh[C::NST][8];   // per page of a tile: s_k (-1: no page), s_v
   __shared__ float q_unit[2][G];                        // score scale of a head, by item parity
-  __shared__ float red[4][2 * G];
-  __shared__ int merge_last;
+  __shared__ float red[4][G], sum_sh[4][G];             // per warp: maxima of a tile, sums of an item
+  __shared__ int2 merge_sh[2];                          // merge task (-1: no more), kv head
 
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* gen = smem_raw + (base - smem_u32(smem_raw));
@@ -124,7 +131,7 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
   const int hkv = prm.num_qo_heads / G;
 
   auto item_at = [&](int n, int& idx) {
-    if (!mbar_wait_bounded(smem_u32(&bars.item_full[n % kItemRing]), (n / kItemRing) & 1, limit,
+    if (!mbar_sleep_bounded(smem_u32(&bars.item_full[n % kItemRing]), (n / kItemRing) & 1, limit,
                            &abort_flag))
       return false;
     idx = *reinterpret_cast<volatile int*>(&item_ring[n % kItemRing]);
@@ -153,6 +160,8 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
       mbar_init(smem_u32(&bars.s_full[s]), 1);
       mbar_init(smem_u32(&bars.p_full[s]), 4);
       mbar_init(smem_u32(&bars.pv_done[s]), 1);
+      mbar_init(smem_u32(&bars.m_full[s]), 4);
+      mbar_init(smem_u32(&bars.m_empty[s]), 1);
     }
     mbar_init(smem_u32(&bars.drain), 1);
     abort_flag = 0;
@@ -182,7 +191,7 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
     const uint32_t box = uint32_t(P) * C::ROWB;
     auto publish = [&](int n, int value) {
       if (n >= kItemRing &&
-          !mbar_wait_bounded(smem_u32(&bars.item_empty[n % kItemRing]), ((n / kItemRing) & 1) ^ 1,
+          !mbar_sleep_bounded(smem_u32(&bars.item_empty[n % kItemRing]), ((n / kItemRing) & 1) ^ 1,
                              limit, &abort_flag))
         return false;
       item_ring[n % kItemRing] = value;
@@ -236,7 +245,7 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
           next_page = prm.page_indices[wn.page_begin + lane];
         }
         const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, valid))) * C::DB * box;
-        if (g >= C::NST && !mbar_wait_warp(smem_u32(&bars.empty[st]), ((g / C::NST) & 1) ^ 1, limit,
+        if (g >= C::NST && !mbar_sleep_warp(smem_u32(&bars.empty[st]), ((g / C::NST) & 1) ^ 1, limit,
                                            &abort_flag)) {
           ok = false;
           break;
@@ -292,7 +301,7 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
       int g = 0;
       auto scores = [&](int q_buf) {     // S of tile g
         const int st = g % C::NST;
-        if (!mbar_wait_bounded(smem_u32(&bars.k_full[st]), (g / C::NST) & 1, limit, &abort_flag))
+        if (!mbar_sleep_bounded(smem_u32(&bars.k_full[st]), (g / C::NST) & 1, limit, &abort_flag))
           return false;
         tc_fence_after();
         const uint64_t kd = kd0 + uint64_t((st * C::STAGE) >> 4);
@@ -308,8 +317,8 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
       };
       auto outputs = [&](int t, bool first) {   // O += V^T P^T of tile t
         const int st = t % C::NST;
-        if (!mbar_wait_bounded(smem_u32(&bars.v_full[st]), (t / C::NST) & 1, limit, &abort_flag) ||
-            !mbar_wait_bounded(smem_u32(&bars.p_full[t & 1]), (t >> 1) & 1, limit, &abort_flag))
+        if (!mbar_sleep_bounded(smem_u32(&bars.v_full[st]), (t / C::NST) & 1, limit, &abort_flag) ||
+            !mbar_sleep_bounded(smem_u32(&bars.p_full[t & 1]), (t >> 1) & 1, limit, &abort_flag))
           return false;
         tc_fence_after();
         const uint64_t vd = vd0 + uint64_t((st * C::STAGE) >> 4);
@@ -328,190 +337,266 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
         tc_commit(smem_u32(&bars.pv_done[t & 1]));
         return true;
       };
-      int pending = -1;          // tile whose output MMAs are still to be issued
-      bool pending_first = false;
       for (int n = 0; ok; ++n) {
         int it = -1;
         ok = item_at(n, it);
         item_done(n);
         if (!ok || it < 0) break;
         const int nt = tiles_of(prm.items[it]);
-        // the previous item's last output does not wait for this item's q
-        if (pending >= 0) {
-          ok = outputs(pending, pending_first);
-          pending = -1;
-          if (!ok) break;
-        }
-        ok = mbar_wait_bounded(smem_u32(&bars.q_full[n & 1]), (n >> 1) & 1, limit, &abort_flag);
+        ok = mbar_sleep_bounded(smem_u32(&bars.q_full[n & 1]), (n >> 1) & 1, limit, &abort_flag);
         for (int j = 0; ok && j < nt; ++j, ++g) {
           ok = scores(n & 1);
-          if (ok && pending >= 0) ok = outputs(pending, pending_first);
-          pending = g;
-          pending_first = j == 0;
+          if (ok && j > 0) ok = outputs(g - 1, j == 1);
         }
+        if (ok && nt > 0) ok = outputs(g - 1, nt == 1);
       }
-      if (ok && pending >= 0) ok = outputs(pending, pending_first);
       if (!ok) {
         abort_flag = 1;
         atomicOr(prm.err, kErrTimeout);
       }
       // every MMA issued so far completes before the TMEM is released
       tc_commit(smem_u32(&bars.drain));
-      mbar_wait_bounded(smem_u32(&bars.drain), 0, limit, nullptr);
+      mbar_sleep_bounded(smem_u32(&bars.drain), 0, limit, nullptr);
     }
     __syncwarp();
+  } else if (warp == 6) {
+    // ----------------------------------------------------------------- merging
+    // The CTA whose chunk completes a row merges the row's states in slot order
+    // (whichever CTA that is, the result is the same).
+    constexpr int V = D / 32;   // dimensions per lane
+    for (int k = 0;; ++k) {
+      // (nothing may be split for as long as the whole launch takes)
+      if (!mbar_sleep_warp(smem_u32(&bars.m_full[k & 1]), (k >> 1) & 1, 64 * limit, &abort_flag)) break;
+      const int2 e = merge_sh[k & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.m_empty[k & 1]));
+      if (e.x < 0) break;
+      const MergeTask mt = prm.merges[e.x];
+      uint32_t before = 0;
+      if (lane == 0) {
+        __threadfence();   // this CTA's states, before the count
+        before = atomicAdd(&prm.merge_counters[e.x * hkv + e.y], 1u);
+        __threadfence();   // and the other CTAs' states after it
+      }
+      before = __shfl_sync(0xffffffffu, before, 0);
+      if (before != uint32_t(mt.n_states - 1)) continue;
+      const size_t row = size_t(mt.out_row) * prm.num_qo_heads + e.y * G;
+      for (int h = 0; h < G; ++h) {
+        const size_t s0 = size_t(mt.slot_base) * prm.num_qo_heads + e.y * G + h;
+        const size_t step = size_t(prm.num_qo_heads);
+        float top = -INFINITY;
+        bool nan = false;      // (fmaxf passes over a NaN)
+        for (int i = lane; i < mt.n_states; i += 32) {
+          const float x = __ldcg(&prm.partial_lse[s0 + i * step]);
+          nan |= x != x;
+          top = fmaxf(top, x);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        float sum = 0.f, acc[V] = {};
+        if (__any_sync(0xffffffffu, nan)) {
+          top = -INFINITY;
+          sum = __uint_as_float(0x7fc00000u);
+        }
+        for (int i0 = 0; top != -INFINITY && i0 < mt.n_states; i0 += 4) {
+          float wgt[4];
+          float x[4][V];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int i = min(i0 + c, mt.n_states - 1);
+            wgt[c] = __ldcg(&prm.partial_lse[s0 + i * step]);
+            const float* src = prm.partial_o + (s0 + i * step) * D + lane * V;
+            if constexpr (V == 2) {
+              const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+              x[c][0] = y.x; x[c][1] = y.y;
+            } else {
+#pragma unroll
+              for (int v = 0; v < V; v += 4) {
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(src + v));
+                x[c][v] = y.x; x[c][v + 1] = y.y; x[c][v + 2] = y.z; x[c][v + 3] = y.w;
+              }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float f = i0 + c < mt.n_states ? ex2((wgt[c] - top) * kLog2e) : 0.f;
+            if (f == 0.f) continue;   // (a state without keys)
+            sum += f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = fmaf(f, x[c][v], acc[v]);
+          }
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(prm.out) +
+                                                    (row + h) * D + lane * V);
+#pragma unroll
+        for (int v = 0; v < V; v += 2) dst[v / 2] = E::pack2(acc[v] * inv, acc[v + 1] * inv);   // (0 * NaN where a state is NaN)
+        if (lane == 0 && prm.lse) prm.lse[row + h] = sum == 0.f ? -INFINITY : top + lg2(sum) * kLn2;
+      }
+    }
   } else {
     // ------------------------------------------------------ softmax + epilogue
     const int t = threadIdx.x;                          // key of the tile, then dimension
     const uint32_t lane_off = uint32_t(warp * 32) << 16;
     const float scale0 = prm.sm_scale * kLog2e;
-    // The four warps meet at named barriers, so none of them leaves alone: a
-    // wait that runs out sets `ok` to false and the next vote ends all four.
+    // The four warps meet at named barriers, so none of them leaves alone: after
+    // a wait that ran out (`ok` false; no wait waits any more) a warp goes on,
+    // and the vote at the next item's start ends all four.
     bool ok = true;
     int g = 0;
     auto sync4 = [] { named_bar_sync(1, 128); };
-    auto all_ok = [&] { return !named_bar_or(1, 128, !ok); };
     auto wait = [&](uint64_t& bar, uint32_t parity) {
-      const bool good = mbar_wait_warp(smem_u32(&bar), parity, limit, &abort_flag);
-      if (!good) ok = false;
-      return good;
+      if (ok && !mbar_sleep_warp(smem_u32(&bar), parity, limit, &abort_flag)) {
+        ok = false;
+        abort_flag = 1;
+      }
     };
-    for (int n = 0;; ++n) {
+    auto take = [&](int n) {
       int it = -1;
-      if (lane == 0) {
+      if (ok && lane == 0) {
         ok = item_at(n, it);
         item_done(n);
       }
-      it = __shfl_sync(0xffffffffu, it, 0);
       ok = __shfl_sync(0xffffffffu, ok, 0) != 0;
-      if (!all_ok()) {
-        ok = false;
-        break;
-      }
-      if (it < 0) break;
-      const WorkItem w = prm.items[it];
-      const int nt = tiles_of(w), lead = lead_of(w);
-      // ---- q as e4m3 terms: warp i takes heads i and i + 4
-      if (nt == 0) {
-        if (lane == 0) mbar_arrive(smem_u32(&bars.q_full[n & 1]));
-      } else {
+      return __shfl_sync(0xffffffffu, it, 0);
+    };
+    // q: warp i loads heads i and i + 4, DPL elements per lane
+    using QWord = typename std::conditional<C::DPL == 8, uint4,
+                                            typename std::conditional<C::DPL == 4, uint2, uint32_t>::type>::type;
+    QWord qw[C::HPW];
+    auto load_q = [&](const WorkItem& w) {
 #pragma unroll
-        for (int h = warp; h < G; h += 4) {
-          const uint16_t* src = reinterpret_cast<const uint16_t*>(prm.q) +
-                                (size_t(w.q_row) * prm.num_qo_heads + w.head * G + h) * D +
-                                lane * C::DPL;
-          float x[C::DPL];
-          if constexpr (C::DPL == 8) {
-            unpack8<E>(*reinterpret_cast<const uint4*>(src), x);
-          } else if constexpr (C::DPL == 4) {
-            const uint2 u = *reinterpret_cast<const uint2*>(src);
-            x[0] = E::lo(u.x); x[1] = E::hi(u.x); x[2] = E::lo(u.y); x[3] = E::hi(u.y);
-          } else {
-            const uint32_t u = *reinterpret_cast<const uint32_t*>(src);
-            x[0] = E::lo(u); x[1] = E::hi(u);
-          }
-          float a = 0.f;
+      for (int x = 0; x < C::HPW; ++x)
+        if (warp + 4 * x < G)
+          qw[x] = *reinterpret_cast<const QWord*>(
+              reinterpret_cast<const uint16_t*>(prm.q) +
+              (size_t(w.q_row) * prm.num_qo_heads + w.head * G + warp + 4 * x) * D + lane * C::DPL);
+    };
+    // ... and writes them as e4m3 terms into the q buffer of item n
+    auto write_q = [&](int n) {
 #pragma unroll
-          for (int e = 0; e < C::DPL; ++e) {
-            const float b = fabsf(x[e]);
-            a = b < INFINITY ? fmaxf(a, b) : a;
-          }
-          a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
-          const uint32_t u = __float_as_uint(a);
-          // the smallest k >= -100 with a <= 448 * 2^k
-          const int k = max(int(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
-          const float inv = pow2i(-k);
-#pragma unroll
-          for (int e = 0; e < C::DPL; ++e)   // (the conversion saturates infinities: NaN instead)
-            x[e] = fabsf(x[e]) < INFINITY ? x[e] * inv : __uint_as_float(0x7fc00000u);
-          const int off = lane * C::DPL, slice = off / 128, byte = off % C::ROWB;
-#pragma unroll
-          for (int tm = 0; tm < C::TERMS; ++tm) {
-            const int row = tm * G + h;
-            const int sw = C::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
-            uint8_t* dst = gen + C::OFF_Q + (n & 1) * C::QBYTES + slice * C::N * C::ROWB +
-                           row * C::ROWB + (((byte >> 4) ^ sw) << 4) + (byte & 15);
-            uint32_t code[(C::DPL + 3) / 4];
-#pragma unroll
-            for (int e = 0; e < C::DPL; e += 2) {
-              const uint32_t c = E4m3::from_f32x2(x[e], x[e + 1]);
-              const uint32_t f = E4m3::to_f16x2(c);
-              x[e] = (x[e] - Fp16::lo(f)) * 16.f;
-              x[e + 1] = (x[e + 1] - Fp16::hi(f)) * 16.f;
-              if (e % 4 == 0) code[e / 4] = c;
-              else code[e / 4] |= c << 16;
-            }
-            if constexpr (C::DPL == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
-            else if constexpr (C::DPL == 4) *reinterpret_cast<uint32_t*>(dst) = code[0];
-            else *reinterpret_cast<uint16_t*>(dst) = uint16_t(code[0]);
-          }
-          if (lane == 0) q_unit[n & 1][h] = scale0 * pow2i(k);
+      for (int y = 0; y < C::HPW; ++y) {
+        const int h = warp + 4 * y;
+        if (h >= G) break;
+        float x[C::DPL];
+        if constexpr (C::DPL == 8) {
+          unpack8<E>(qw[y], x);
+        } else if constexpr (C::DPL == 4) {
+          x[0] = E::lo(qw[y].x); x[1] = E::hi(qw[y].x); x[2] = E::lo(qw[y].y); x[3] = E::hi(qw[y].y);
+        } else {
+          x[0] = E::lo(qw[y]); x[1] = E::hi(qw[y]);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.q_full[n & 1]));
-        sync4();   // q_unit of every head
+        float a = 0.f;
+#pragma unroll
+        for (int e = 0; e < C::DPL; ++e) {
+          const float b = fabsf(x[e]);
+          a = b < INFINITY ? fmaxf(a, b) : a;
+        }
+        a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+        const uint32_t u = __float_as_uint(a);
+        // the smallest k >= -100 with a <= 448 * 2^k
+        const int k = max(int(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+        const float inv = pow2i(-k);
+#pragma unroll
+        for (int e = 0; e < C::DPL; ++e)   // (the conversion saturates infinities: NaN instead)
+          x[e] = fabsf(x[e]) < INFINITY ? x[e] * inv : __uint_as_float(0x7fc00000u);
+        const int off = lane * C::DPL, slice = off / 128, byte = off % C::ROWB;
+#pragma unroll
+        for (int tm = 0; tm < C::TERMS; ++tm) {
+          const int row = tm * G + h;
+          const int sw = C::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
+          uint8_t* dst = gen + C::OFF_Q + (n & 1) * C::QBYTES + slice * C::N * C::ROWB +
+                         row * C::ROWB + (((byte >> 4) ^ sw) << 4) + (byte & 15);
+          uint32_t code[(C::DPL + 3) / 4];
+#pragma unroll
+          for (int e = 0; e < C::DPL; e += 2) {
+            const uint32_t c = E4m3::from_f32x2(x[e], x[e + 1]);
+            const uint32_t f = E4m3::to_f16x2(c);
+            x[e] = (x[e] - Fp16::lo(f)) * 16.f;
+            x[e + 1] = (x[e + 1] - Fp16::hi(f)) * 16.f;
+            if (e % 4 == 0) code[e / 4] = c;
+            else code[e / 4] |= c << 16;
+          }
+          if constexpr (C::DPL == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
+          else if constexpr (C::DPL == 4) *reinterpret_cast<uint32_t*>(dst) = code[0];
+          else *reinterpret_cast<uint16_t*>(dst) = uint16_t(code[0]);
+        }
+        if (lane == 0) q_unit[n & 1][h] = scale0 * pow2i(k);
       }
-      float unit[G], m[G], mu[G], l[G];
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.q_full[n & 1]));
+    };
+    int it = take(0), merges = 0;
+    WorkItem w;
+    if (it >= 0) {
+      w = prm.items[it];
+      load_q(w);
+      write_q(0);
+    }
+    for (int n = 0;; ++n) {
+      // (also: q_unit of every head is there)
+      ok = !named_bar_or(1, 128, !ok);
+      if (!ok || it < 0) break;
+      const int it_next = take(n + 1);
+      WorkItem wn;
+      if (it_next >= 0) wn = prm.items[it_next];
+      const int nt = tiles_of(w), lead = lead_of(w);
+      float unit[G], m[G], l[G];
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        unit[h] = nt > 0 ? q_unit[n & 1][h] : 0.f;
-        m[h] = mu[h] = -INFINITY;
+        unit[h] = q_unit[n & 1][h];
+        m[h] = -INFINITY;
         l[h] = 0.f;
       }
+      float ref = 1.f;   // r
+      if (nt == 0 && it_next >= 0) load_q(wn);
       for (int j = 0; j < nt; ++j, ++g) {
         const int st = g % C::NST;
         // this key's page scales
         wait(bars.k_full[st], (g / C::NST) & 1);
         const float2 sc = scale_sh[st][t / P];
+        if (j == 0) {
+          const float2 s0 = scale_sh[st][0];
+          ref = s0.x < 0.f ? 1.f : s0.y;
+        }
         const int i = j * C::T + t - lead;              // key number from tok_begin
         const bool seen = i >= 0 && i < w.tok_end - w.tok_begin && sc.x >= 0.f;
-        const float lv = lg2(sc.y);
+        const float lv = lg2(sc.y), per_v = fminf(__fdividef(ref, sc.y), 1.2676506e30f);
         wait(bars.s_full[g & 1], (g >> 1) & 1);
         tc_fence_after();
         uint32_t r[C::N];
         if constexpr (C::N == 16) tmem_ld16(tmem + lane_off + (g & 1) * C::N, r);
         else tmem_ld32(tmem + lane_off + (g & 1) * C::N, r);
         tmem_wait_ld();
-        float s[G];
+        float u[G];      // score + log2 s_v
         bool grow = false;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           float x = __uint_as_float(r[h]);
           x = fmaf(__uint_as_float(r[G + h]), 0.0625f, x);
           if (C::TERMS == 3) x = fmaf(__uint_as_float(r[2 * G + h]), 0.00390625f, x);
-          s[h] = seen ? x * (sc.x * unit[h]) : -INFINITY;
-          grow |= s[h] > m[h] + kGrow || s[h] + lv > mu[h] + kGrow;
+          u[h] = seen ? fmaf(x, sc.x * unit[h], lv) : -INFINITY;
+          grow |= u[h] > m[h] + kGrow;
         }
-        if (named_bar_or(1, 128, grow || !ok)) {
+        if (named_bar_or(1, 128, grow)) {
           // new maxima over the tile's keys, and O and l on the new scale
 #pragma unroll
           for (int h = 0; h < G; ++h) {
-            // (NaN scores leave the maxima alone)
-            const float a = warp_max(s[h] == s[h] ? s[h] : -INFINITY);
-            const float b = warp_max(s[h] + lv == s[h] + lv ? s[h] + lv : -INFINITY);
-            if (lane == 0) {
-              red[warp][h] = a;
-              red[warp][G + h] = b;
-            }
+            const float a = warp_max(u[h] == u[h] ? u[h] : -INFINITY);   // (without NaN)
+            if (lane == 0) red[warp][h] = a;
           }
-          if (!all_ok()) {
-            ok = false;
-            break;
-          }
+          sync4();
           float alpha[G];
           bool live = false;
 #pragma unroll
           for (int h = 0; h < G; ++h) {
             const float a = fmaxf(fmaxf(red[0][h], red[1][h]), fmaxf(red[2][h], red[3][h]));
-            const float b = fmaxf(fmaxf(red[0][G + h], red[1][G + h]),
-                                  fmaxf(red[2][G + h], red[3][G + h]));
-            const float m2 = fmaxf(m[h], a), mu2 = fmaxf(mu[h], b);
-            l[h] *= m[h] == -INFINITY ? 0.f : ex2(m[h] - m2);
-            alpha[h] = mu[h] == -INFINITY ? 0.f : ex2(mu[h] - mu2);
+            const float m2 = fmaxf(m[h], a);
+            alpha[h] = m[h] == -INFINITY ? 0.f : ex2(m[h] - m2);
+            l[h] *= alpha[h];
             live |= alpha[h] != 1.f;
             m[h] = m2;
-            mu[h] = mu2;
           }
           if (j > 0 && live) {
             wait(bars.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
@@ -532,7 +617,7 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
             tmem_wait_st();
           }
         }
-        // weights: p = 2^(s - m) into the sums, p s_v as e4m3 terms into P^T
+        // weights, as e4m3 terms into P^T
         uint32_t pw[C::N / 4];
 #pragma unroll
         for (int c = 0; c < C::N / 4; ++c) pw[c] = 0u;
@@ -541,8 +626,9 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
           float x[2] = {0.f, 0.f};
 #pragma unroll
           for (int e = 0; e < 2 && h + e < G; ++e) {
-            l[h + e] += ex2(s[h + e] - (m[h + e] == -INFINITY ? 0.f : m[h + e]));
-            x[e] = kWeightUnit * ex2(s[h + e] + lv - (mu[h + e] == -INFINITY ? 0.f : mu[h + e]));
+            x[e] = ex2(u[h + e] - (m[h + e] == -INFINITY ? 0.f : m[h + e]));
+            l[h + e] = fmaf(x[e], per_v, l[h + e]);
+            x[e] *= kWeightUnit;
           }
 #pragma unroll
           for (int tm = 0; tm < C::TERMS; ++tm) {
@@ -568,7 +654,8 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
         // V rows of keys outside the item hold stale bytes, maybe NaN codes,
         // which a zero weight would not cancel
         if (__any_sync(0xffffffffu, !seen)) {
-          if (wait(bars.v_full[st], (g / C::NST) & 1) && !seen) {
+          wait(bars.v_full[st], (g / C::NST) & 1);
+          if (!seen) {
 #pragma unroll
             for (int b = 0; b < C::DB; ++b)
 #pragma unroll
@@ -580,32 +667,28 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[g & 1]));
+        if (j == 0 && it_next >= 0) load_q(wn);   // (its work item is there by now)
       }
-      // ---- epilogue: out = O 2^(mu - m) / (unit sum p), lse = ln 2 (m + log2 sum p)
-      if (ok && nt > 0) wait(bars.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
-      if (!all_ok()) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
+      if (it_next >= 0) write_q(n + 1);
+      // ---- epilogue: the sums of the four warps' keys
 #pragma unroll
       for (int h = 0; h < G; ++h) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
-        if (lane == 0) red[warp][h] = l[h];
+        if (lane == 0) sum_sh[warp][h] = l[h];
       }
       sync4();
       float f[G];
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        l[h] = (red[0][h] + red[1][h]) + (red[2][h] + red[3][h]);
+        l[h] = (sum_sh[0][h] + sum_sh[1][h]) + (sum_sh[2][h] + sum_sh[3][h]);
         // (a NaN sum, from a NaN in q or in the cache, stays one)
-        f[h] = l[h] == 0.f ? 0.f
-                           : prm.v_scale * ex2(mu[h] == -INFINITY ? 0.f : mu[h] - m[h]) /
-                                 (kWeightUnit * l[h]);
+        f[h] = l[h] == 0.f ? 0.f : prm.v_scale * ref / (kWeightUnit * l[h]);
       }
       const bool split = w.slot >= 0;
       const size_t orow = size_t(split ? w.slot : w.q_row) * prm.num_qo_heads + w.head * G;
+      if (nt > 0) wait(bars.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+      tc_fence_after();
 #pragma unroll
       for (int b = 0; b < C::DB; ++b) {
         uint32_t o[C::N];
@@ -618,7 +701,7 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
 #pragma unroll
           for (int c = 0; c < C::N; ++c) o[c] = 0u;
         }
-        if (t < D) {
+        if (t < D && ok) {
 #pragma unroll
           for (int h = 0; h < G; ++h) {
             float x = __uint_as_float(o[h]);
@@ -633,51 +716,30 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
       }
       float* lse = split ? prm.partial_lse : prm.lse;
       if (lse) {
+        const float lr = lg2(ref);
 #pragma unroll
         for (int h = 0; h < G; ++h)
-          if (t == h) lse[orow + h] = l[h] == 0.f ? -INFINITY : (m[h] + lg2(l[h])) * kLn2;
+          if (t == h) lse[orow + h] = l[h] == 0.f ? -INFINITY : (m[h] + (lg2(l[h]) - lr)) * kLn2;
       }
       tc_fence_before();
-      sync4();   // red is free again
       if (split) {
-        // the CTA that finishes a row's last chunk merges its states, in slot order
-        const MergeTask mt = prm.merges[w.merge];
-        __threadfence();
-        sync4();
-        if (t == 0) {
-          merge_last = atomicAdd(&prm.merge_counters[w.merge * hkv + w.head], 1u) ==
-                       uint32_t(mt.n_states - 1);
-          if (merge_last) __threadfence();
-        }
-        sync4();
-        if (*reinterpret_cast<volatile int*>(&merge_last)) {
-          const size_t row = size_t(mt.out_row) * prm.num_qo_heads + w.head * G;
-          for (int h = 0; h < G; ++h) {
-            const size_t s0 = size_t(mt.slot_base) * prm.num_qo_heads + w.head * G + h;
-            float top = -INFINITY;
-            for (int i = 0; i < mt.n_states; ++i)
-              top = fmaxf(top, __ldcg(&prm.partial_lse[s0 + size_t(i) * prm.num_qo_heads]));
-            float sum = 0.f, acc[C::DB];
-#pragma unroll
-            for (int b = 0; b < C::DB; ++b) acc[b] = 0.f;
-            for (int i = 0; top != -INFINITY && i < mt.n_states; ++i) {
-              const size_t at = s0 + size_t(i) * prm.num_qo_heads;
-              const float wgt = ex2((__ldcg(&prm.partial_lse[at]) - top) * kLog2e);
-              sum += wgt;
-#pragma unroll
-              for (int b = 0; b < C::DB; ++b)
-                if (t < D) acc[b] = fmaf(wgt, __ldcg(&prm.partial_o[at * D + b * 128 + t]), acc[b]);
-            }
-#pragma unroll
-            for (int b = 0; b < C::DB; ++b)
-              if (t < D)
-                reinterpret_cast<uint16_t*>(prm.out)[(row + h) * D + b * 128 + t] =
-                    E::one(sum == 0.f ? 0.f : acc[b] / sum);
-            if (t == 0 && prm.lse)
-              prm.lse[row + h] = sum == 0.f ? -INFINITY : top + lg2(sum) * kLn2;
-          }
-        }
+        const int e = merges & 1;
+        if (merges >= 2) wait(bars.m_empty[e], ((merges - 2) >> 1) & 1);
+        if (t == 0) merge_sh[e] = make_int2(w.merge, w.head);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.m_full[e]));
+        ++merges;
       }
+      w = wn;
+      it = it_next;
+    }
+    // no more merges
+    {
+      const int e = merges & 1;
+      if (merges >= 2) wait(bars.m_empty[e], ((merges - 2) >> 1) & 1);
+      if (t == 0) merge_sh[e] = make_int2(-1, 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.m_full[e]));
     }
     if (!ok && lane == 0) {
       abort_flag = 1;
@@ -695,8 +757,8 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
   if (warp == 4 && lane == 0) {
     for (int j = max(0, issued - C::NST); j < issued; ++j) {
       if (!(j == 0 && prm.fault_kind == 1 && blockIdx.x == 0))   // K never issued
-        mbar_wait_bounded(smem_u32(&bars.k_full[j % C::NST]), (j / C::NST) & 1, limit, nullptr);
-      mbar_wait_bounded(smem_u32(&bars.v_full[j % C::NST]), (j / C::NST) & 1, limit, nullptr);
+        mbar_sleep_bounded(smem_u32(&bars.k_full[j % C::NST]), (j / C::NST) & 1, limit, nullptr);
+      mbar_sleep_bounded(smem_u32(&bars.v_full[j % C::NST]), (j / C::NST) & 1, limit, nullptr);
     }
   }
 }

@@ -411,3 +411,19 @@ def test_decode_many_items_of_few_keys(g, d, dtype):
         dv.run()
         assert torch.equal(dv.out, o1) and torch.equal(dv.lse, l1)
         assert dv.status() == B.FI_OK
+
+
+def test_decode_nan_rows_of_split_requests_stay_nan():
+    import torch
+    b = _page8.Batch([3000, 5000, 40], 8, 2, 128, 16, seed=34)
+    _check(b, 152, what="split")
+    b.q[0, 1, 5] = float("nan")
+    b.q[1, 6, 0] = float("inf")
+    d = _page8.Device(b, 152)
+    assert B.fi_plan_get_info(d.plan)["num_split_requests"] == 2
+    out, lse = d.run()
+    want = np.zeros((3, 8), dtype=bool)
+    want[0, 1] = want[1, 6] = True
+    assert np.array_equal(torch.isnan(out).all(dim=2).cpu().numpy(), want)
+    assert np.array_equal(torch.isnan(out).any(dim=2).cpu().numpy(), want)
+    assert np.array_equal(torch.isnan(lse).cpu().numpy(), want)
