@@ -26,14 +26,14 @@
 // one exponential per score, and both sums keep their leading bits whatever
 // the spread of the scales.
 //
-// Roles (7 warps): 0-3 softmax (thread = key of the tile = TMEM lane), then
+// Roles (8 warps): 0-3 softmax (thread = key of the tile = TMEM lane), then
 // the epilogue (thread = dimension); 4 copies pages by TMA and page scales by
 // cp.async into a ring; 5 issues the MMAs (the scores of tile j + 1 before the
 // output of tile j, with two score buffers); 6 merges the states of requests
-// whose last chunk this CTA finished, beside the next items. The launch is
-// persistent: a CTA takes items from a counter, the ring runs on from item to
-// item, and an item's q is loaded and turned into terms before the previous
-// item's epilogue (an item's start and end had cost as much as four tiles).
+// whose last chunk this CTA finished, beside the next items; 7 turns the next
+// item's q into terms. The launch is persistent: a CTA takes items from a
+// counter and the ring runs on from item to item. (With q and the merge on the
+// softmax warps, an item's start and end cost as much as four tiles.)
 #include <cfloat>
 #include <type_traits>
 
@@ -76,12 +76,10 @@ struct D8Cfg {
   static constexpr int OFF_Q = NST * STAGE;                 // two buffers
   static constexpr int OFF_P = OFF_Q + 2 * QBYTES;          // two buffers
   static constexpr int SMEM = OFF_P + 2 * PBYTES + 1024;
-  static constexpr int THREADS = 224;
+  static constexpr int THREADS = 256;
   static constexpr uint32_t TMEM_COLS = N * (2 + DB) <= 64 ? 64 : 128;
   static constexpr uint32_t IDESC_S = idesc_e4m3(128, N, 0, 0);
   static constexpr uint32_t IDESC_O = idesc_e4m3(128, 16, 1, 1);
-  static constexpr int DPL = D / 32;                        // q elements per lane and head
-  static constexpr int HPW = (G + 3) / 4;                   // heads whose q a softmax warp loads
   static_assert(SMEM * CTAS <= 227 * 1024, "shared-memory budget");
   static_assert(COLS <= 32 && N * (2 + DB) <= 128, "");
 };
@@ -89,7 +87,7 @@ struct D8Cfg {
 struct D8Barriers {
   uint64_t item_full[kItemRing], item_empty[kItemRing];
   uint64_t k_full[6], v_full[6], empty[6];
-  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
   uint64_t m_full[2], m_empty[2];   // finished chunks for the merging warp
   uint64_t drain;
 };
@@ -117,7 +115,7 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
   __shared__ __align__(8) D8Barriers bars;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
-  __shared__ int item_ring[kItemRing];
+  __shared__ WorkItem item_ring[kItemRing];             // req < 0: no more
   __shared__ __align__(8) float2 scale_sh[C::NST][8];   // per page of a tile: s_k (-1: no page), s_v
   __shared__ float q_unit[2][G];                        // score scale of a head, by item parity
   __shared__ float red[4][G], sum_sh[4][G];             // per warp: maxima of a tile, sums of an item
@@ -130,14 +128,20 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
   const int P = prm.page_size, ppt = C::T / P;
   const int hkv = prm.num_qo_heads / G;
 
-  auto item_at = [&](int n, int& idx) {
+  // item n of this CTA (for a whole warp, or for one thread)
+  auto take_item = [&](int n, WorkItem& w) {
     if (!mbar_sleep_bounded(smem_u32(&bars.item_full[n % kItemRing]), (n / kItemRing) & 1, limit,
-                           &abort_flag))
+                            &abort_flag))
       return false;
-    idx = *reinterpret_cast<volatile int*>(&item_ring[n % kItemRing]);
+    w = item_ring[n % kItemRing];
     return true;
   };
-  auto item_done = [&](int n) { mbar_arrive(smem_u32(&bars.item_empty[n % kItemRing])); };
+  auto take_item_warp = [&](int n, WorkItem& w) {
+    const bool good = take_item(n, w);
+    if (!__all_sync(0xffffffffu, good)) return false;
+    if (lane == 0) mbar_arrive(smem_u32(&bars.item_empty[n % kItemRing]));
+    return true;
+  };
   // tiles of an item: its keys from the start of its first page
   auto lead_of = [&](const WorkItem& w) { return w.tok_begin % P; };
   auto tiles_of = [&](const WorkItem& w) {
@@ -148,7 +152,7 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
   if (threadIdx.x == 0) {
     for (int s = 0; s < kItemRing; ++s) {
       mbar_init(smem_u32(&bars.item_full[s]), 1);
-      mbar_init(smem_u32(&bars.item_empty[s]), 5);      // 4 softmax warps, the MMA warp
+      mbar_init(smem_u32(&bars.item_empty[s]), 6);      // 4 softmax warps, the MMA and q warps
     }
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(smem_u32(&bars.k_full[s]), 1 + ppt);    // K's bytes, and each page's scales
@@ -156,7 +160,8 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
       mbar_init(smem_u32(&bars.empty[s]), 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&bars.q_full[s]), 4);
+      mbar_init(smem_u32(&bars.q_full[s]), 1);
+      mbar_init(smem_u32(&bars.q_empty[s]), 5);         // the last scores; the 4 softmax warps
       mbar_init(smem_u32(&bars.s_full[s]), 1);
       mbar_init(smem_u32(&bars.p_full[s]), 4);
       mbar_init(smem_u32(&bars.pv_done[s]), 1);
@@ -189,47 +194,47 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
       prefetch_tensormap(&v_map);
     }
     const uint32_t box = uint32_t(P) * C::ROWB;
-    auto publish = [&](int n, int value) {
-      if (n >= kItemRing &&
-          !mbar_sleep_bounded(smem_u32(&bars.item_empty[n % kItemRing]), ((n / kItemRing) & 1) ^ 1,
-                             limit, &abort_flag))
+    // The next item is taken in three steps with copies in between, so that the
+    // latencies of the counter and of the work list hide behind them.
+    int v_next = 0;
+    auto count = [&] {
+      if (lane == 0) v_next = int(gridDim.x + atomicAdd(prm.work_counter, 1u));
+    };
+    auto look_up = [&](int v, WorkItem& w) {
+      if (v < prm.n_items) w = prm.items[v];
+      else w.req = -1;
+    };
+    auto publish = [&](int n, const WorkItem& w) {   // as item n of this CTA
+      if (n >= kItemRing && !mbar_sleep_warp(smem_u32(&bars.item_empty[n % kItemRing]),
+                                             ((n / kItemRing) & 1) ^ 1, limit, &abort_flag))
         return false;
-      item_ring[n % kItemRing] = value;
-      mbar_arrive(smem_u32(&bars.item_full[n % kItemRing]));
+      if (lane == 0) {
+        item_ring[n % kItemRing] = w;
+        mbar_arrive(smem_u32(&bars.item_full[n % kItemRing]));
+      }
       return true;
     };
-    auto next_item = [&](int n, int& idx) {   // item n of this CTA, published
-      int v = -1;
-      bool good = true;
-      if (lane == 0) {
-        v = n == 0 ? int(blockIdx.x) : int(gridDim.x + atomicAdd(prm.work_counter, 1u));
-        if (v >= prm.n_items) v = -1;
-        good = publish(n, v);
-      }
-      idx = __shfl_sync(0xffffffffu, v, 0);
-      return __shfl_sync(0xffffffffu, good, 0) != 0;
-    };
     auto pages_in = [&](const WorkItem& w, int j) { return min(ppt, w.n_pages - j * ppt); };
-    int it = -1, g = 0;
-    bool ok = next_item(0, it);
-    WorkItem w;
-    if (ok && it >= 0) w = prm.items[it];
+    int g = 0;
+    WorkItem w, wn;
+    look_up(int(blockIdx.x), w);
+    bool ok = publish(0, w);
     int next_page = -1;
-    if (ok && it >= 0 && lane < pages_in(w, 0)) next_page = prm.page_indices[w.page_begin + lane];
-    for (int n = 0; ok && it >= 0; ++n) {
+    if (ok && w.req >= 0 && lane < pages_in(w, 0))
+      next_page = prm.page_indices[w.page_begin + lane];
+    for (int n = 0; ok && w.req >= 0; ++n) {
       const int nt = tiles_of(w);
       const int c1 = prm.layout == FI_LAYOUT_NHD ? w.head : 0;
       const int c2 = prm.layout == FI_LAYOUT_NHD ? 0 : w.head;
-      int it_next = -1;
-      if (!next_item(n + 1, it_next)) {
-        ok = false;
-        break;
-      }
-      WorkItem wn;
-      if (it_next >= 0) wn = prm.items[it_next];
+      auto first_pages = [&] {
+        next_page = wn.req >= 0 && lane < pages_in(wn, 0) ? prm.page_indices[wn.page_begin + lane] : -1;
+      };
+      count();
       if (nt == 0) {
-        next_page = -1;
-        if (it_next >= 0 && lane < pages_in(wn, 0)) next_page = prm.page_indices[wn.page_begin + lane];
+        look_up(__shfl_sync(0xffffffffu, v_next, 0), wn);
+        first_pages();
+        ok = publish(n + 1, wn);
+        if (!ok) break;
       }
       for (int j = 0; j < nt; ++j, ++g) {
         const int st = g % C::NST;
@@ -241,8 +246,8 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
         if (j + 1 < nt) {
           if (lane < pages_in(w, j + 1))
             next_page = prm.page_indices[w.page_begin + (j + 1) * ppt + lane];
-        } else if (it_next >= 0 && lane < pages_in(wn, 0)) {
-          next_page = prm.page_indices[wn.page_begin + lane];
+        } else if (j > 0) {
+          first_pages();
         }
         const uint32_t bytes = uint32_t(__popc(__ballot_sync(0xffffffffu, valid))) * C::DB * box;
         if (g >= C::NST && !mbar_sleep_warp(smem_u32(&bars.empty[st]), ((g / C::NST) & 1) ^ 1, limit,
@@ -278,9 +283,14 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
           }
         }
         issued = g + 1;
+        if (j == 0) look_up(__shfl_sync(0xffffffffu, v_next, 0), wn);
+        if (nt == 1) first_pages();
+        if ((j == 1 || nt == 1) && !publish(n + 1, wn)) {
+          ok = false;
+          break;
+        }
       }
       w = wn;
-      it = it_next;
     }
     if (!ok && lane == 0) {
       abort_flag = 1;
@@ -338,16 +348,19 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
         return true;
       };
       for (int n = 0; ok; ++n) {
-        int it = -1;
-        ok = item_at(n, it);
-        item_done(n);
-        if (!ok || it < 0) break;
-        const int nt = tiles_of(prm.items[it]);
+        WorkItem w;
+        ok = take_item(n, w);
+        if (!ok) break;
+        mbar_arrive(smem_u32(&bars.item_empty[n % kItemRing]));
+        if (w.req < 0) break;
+        const int nt = tiles_of(w);
         ok = mbar_sleep_bounded(smem_u32(&bars.q_full[n & 1]), (n >> 1) & 1, limit, &abort_flag);
         for (int j = 0; ok && j < nt; ++j, ++g) {
           ok = scores(n & 1);
+          if (ok && j + 1 == nt) tc_commit(smem_u32(&bars.q_empty[n & 1]));
           if (ok && j > 0) ok = outputs(g - 1, j == 1);
         }
+        if (ok && nt == 0) mbar_arrive(smem_u32(&bars.q_empty[n & 1]));
         if (ok && nt > 0) ok = outputs(g - 1, nt == 1);
       }
       if (!ok) {
@@ -359,11 +372,99 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
       mbar_sleep_bounded(smem_u32(&bars.drain), 0, limit, nullptr);
     }
     __syncwarp();
+  } else if (warp == 7) {
+    // ----------------------------------------------------------------- q terms
+    const float scale0 = prm.sm_scale * kLog2e;
+    // the g heads' elements are consecutive: 32 / g lanes per head
+    constexpr int LPH = 32 / G, EPL = D / LPH, WORDS = EPL / 2;
+    const int h = lane / LPH, off = lane % LPH * EPL;
+    bool ok = true;
+    for (int n = 0;; ++n) {
+      WorkItem w;
+      ok = take_item_warp(n, w);
+      if (!ok || w.req < 0) break;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          reinterpret_cast<const uint16_t*>(prm.q) +
+          (size_t(w.q_row) * prm.num_qo_heads + w.head * G) * D + lane * EPL);
+      uint32_t u[WORDS];
+      if constexpr (WORDS >= 4) {
+#pragma unroll
+        for (int e = 0; e < WORDS; e += 4) {
+          const uint4 y = *reinterpret_cast<const uint4*>(src + e);
+          u[e] = y.x; u[e + 1] = y.y; u[e + 2] = y.z; u[e + 3] = y.w;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < WORDS; ++e) u[e] = src[e];
+      }
+      if (n >= 2) ok = mbar_sleep_warp(smem_u32(&bars.q_empty[n & 1]), ((n - 2) >> 1) & 1, limit,
+                                       &abort_flag);
+      if (!ok) break;
+      float x[EPL];
+      float a = 0.f;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        x[e] = e % 2 == 0 ? E::lo(u[e / 2]) : E::hi(u[e / 2]);
+        const float b = fabsf(x[e]);
+        a = b < INFINITY ? fmaxf(a, b) : a;
+      }
+#pragma unroll
+      for (int d = LPH / 2; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+      const uint32_t au = __float_as_uint(a);
+      // the smallest k >= -100 with a <= 448 * 2^k
+      const int k = max(int(au >> 23) - 127 - 8 + ((au & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+      const float inv = pow2i(-k);
+#pragma unroll
+      for (int e = 0; e < EPL; ++e)   // (the conversion saturates infinities: NaN instead)
+        x[e] = fabsf(x[e]) < INFINITY ? x[e] * inv : __uint_as_float(0x7fc00000u);
+#pragma unroll
+      for (int tm = 0; tm < C::TERMS; ++tm) {
+        const int row = tm * G + h;
+        const int sw = C::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
+        uint32_t code[(EPL + 3) / 4];
+#pragma unroll
+        for (int e = 0; e < EPL; e += 2) {
+          const uint32_t c = E4m3::from_f32x2(x[e], x[e + 1]);
+          const uint32_t f = E4m3::to_f16x2(c);
+          x[e] = (x[e] - Fp16::lo(f)) * 16.f;
+          x[e + 1] = (x[e + 1] - Fp16::hi(f)) * 16.f;
+          if (e % 4 == 0) code[e / 4] = c;
+          else code[e / 4] |= c << 16;
+        }
+        uint8_t* buf = gen + C::OFF_Q + (n & 1) * C::QBYTES + row * C::ROWB;
+        constexpr int PIECE = EPL < 16 ? EPL : 16;
+#pragma unroll
+        for (int e = 0; e < EPL; e += PIECE) {
+          const int at = off + e, byte = at % C::ROWB;
+          uint8_t* dst = buf + at / 128 * C::N * C::ROWB + (((byte >> 4) ^ sw) << 4) + (byte & 15);
+          if constexpr (PIECE == 16)
+            *reinterpret_cast<uint4*>(dst) =
+                make_uint4(code[e / 4], code[e / 4 + 1], code[e / 4 + 2], code[e / 4 + 3]);
+          else if constexpr (PIECE == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
+          else if constexpr (PIECE == 4) *reinterpret_cast<uint32_t*>(dst) = code[0];
+          else *reinterpret_cast<uint16_t*>(dst) = uint16_t(code[0]);
+        }
+      }
+      if (lane % LPH == 0) q_unit[n & 1][h] = scale0 * pow2i(k);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.q_full[n & 1]));
+    }
+    if (!ok && lane == 0) {
+      abort_flag = 1;
+      atomicOr(prm.err, kErrTimeout);
+    }
   } else if (warp == 6) {
     // ----------------------------------------------------------------- merging
     // The CTA whose chunk completes a row merges the row's states in slot order
-    // (whichever CTA that is, the result is the same).
-    constexpr int V = D / 32;   // dimensions per lane
+    // (whichever CTA that is, the result is the same): all heads at once, 32 / G
+    // states at a time, with a running maximum per head.
+    constexpr int SPB = 32 / G;            // states per block: a lane has one (state, head)'s lse
+    constexpr int NV = (G * D + 127) / 128;   // float4 pieces per lane and state
+    const int h_of = lane % G;
+    const bool has = G * D >= 128 || lane * 4 < G * D;
+    // the head of piece v of this lane
+    auto head_of = [&](int v) { return G == 1 ? 0 : (v * 128 + lane * 4) / D; };
     for (int k = 0;; ++k) {
       // (nothing may be split for as long as the whole launch takes)
       if (!mbar_sleep_warp(smem_u32(&bars.m_full[k & 1]), (k >> 1) & 1, 64 * limit, &abort_flag)) break;
@@ -381,64 +482,69 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
       before = __shfl_sync(0xffffffffu, before, 0);
       if (before != uint32_t(mt.n_states - 1)) continue;
       const size_t row = size_t(mt.out_row) * prm.num_qo_heads + e.y * G;
-      for (int h = 0; h < G; ++h) {
-        const size_t s0 = size_t(mt.slot_base) * prm.num_qo_heads + e.y * G + h;
-        const size_t step = size_t(prm.num_qo_heads);
-        float top = -INFINITY;
-        bool nan = false;      // (fmaxf passes over a NaN)
-        for (int i = lane; i < mt.n_states; i += 32) {
-          const float x = __ldcg(&prm.partial_lse[s0 + i * step]);
-          nan |= x != x;
-          top = fmaxf(top, x);
+      const size_t slot0 = size_t(mt.slot_base) * prm.num_qo_heads + e.y * G;
+      const size_t step = size_t(prm.num_qo_heads);
+      // of head h_of: the maximum of lse, and sum 2^(lse - top) (log2 units)
+      float top = -INFINITY, sum = 0.f;
+      float4 acc[NV];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = 0; i0 < mt.n_states; i0 += SPB) {
+        const int i = i0 + lane / G;
+        const float s = i < mt.n_states ? __ldcg(&prm.partial_lse[slot0 + i * step + h_of]) * kLog2e
+                                        : -INFINITY;
+        float top2 = s == s ? s : INFINITY;      // (a NaN: kept out of fmaxf, see below)
+#pragma unroll
+        for (int d = G; d < 32; d <<= 1) top2 = fmaxf(top2, __shfl_xor_sync(0xffffffffu, top2, d));
+        top2 = fmaxf(top, top2);
+        // 2^(x - x) = NaN for x = inf makes the row NaN; -inf: no keys so far
+        const float old = top == -INFINITY ? (top2 == INFINITY ? top2 - top2 : 0.f) : ex2(top - top2);
+        const float f = top2 == -INFINITY ? 0.f : ex2(s - top2);
+        top = top2;
+        float block = f;
+#pragma unroll
+        for (int d = G; d < 32; d <<= 1) block += __shfl_xor_sync(0xffffffffu, block, d);
+        sum = fmaf(sum, old, block);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const float o = __shfl_sync(0xffffffffu, old, head_of(v));
+          acc[v].x *= o; acc[v].y *= o; acc[v].z *= o; acc[v].w *= o;
         }
+#pragma unroll 2
+        for (int c = 0; c < SPB; ++c) {
+          if (i0 + c >= mt.n_states) break;
+          float4 x[NV];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        float sum = 0.f, acc[V] = {};
-        if (__any_sync(0xffffffffu, nan)) {
-          top = -INFINITY;
-          sum = __uint_as_float(0x7fc00000u);
-        }
-        for (int i0 = 0; top != -INFINITY && i0 < mt.n_states; i0 += 4) {
-          float wgt[4];
-          float x[4][V];
+          for (int v = 0; v < NV; ++v)
+            x[v] = has ? __ldcg(reinterpret_cast<const float4*>(prm.partial_o +
+                                                                (slot0 + (i0 + c) * step) * D) +
+                                v * 32 + lane)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int i = min(i0 + c, mt.n_states - 1);
-            wgt[c] = __ldcg(&prm.partial_lse[s0 + i * step]);
-            const float* src = prm.partial_o + (s0 + i * step) * D + lane * V;
-            if constexpr (V == 2) {
-              const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
-              x[c][0] = y.x; x[c][1] = y.y;
-            } else {
-#pragma unroll
-              for (int v = 0; v < V; v += 4) {
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(src + v));
-                x[c][v] = y.x; x[c][v + 1] = y.y; x[c][v + 2] = y.z; x[c][v + 3] = y.w;
-              }
-            }
+          for (int v = 0; v < NV; ++v) {
+            const float p = __shfl_sync(0xffffffffu, f, c * G + head_of(v));
+            acc[v].x = fmaf(p, x[v].x, acc[v].x);
+            acc[v].y = fmaf(p, x[v].y, acc[v].y);
+            acc[v].z = fmaf(p, x[v].z, acc[v].z);
+            acc[v].w = fmaf(p, x[v].w, acc[v].w);
           }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float f = i0 + c < mt.n_states ? ex2((wgt[c] - top) * kLog2e) : 0.f;
-            if (f == 0.f) continue;   // (a state without keys)
-            sum += f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] = fmaf(f, x[c][v], acc[v]);
-          }
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(prm.out) +
-                                                    (row + h) * D + lane * V);
-#pragma unroll
-        for (int v = 0; v < V; v += 2) dst[v / 2] = E::pack2(acc[v] * inv, acc[v + 1] * inv);   // (0 * NaN where a state is NaN)
-        if (lane == 0 && prm.lse) prm.lse[row + h] = sum == 0.f ? -INFINITY : top + lg2(sum) * kLn2;
       }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const float o = __shfl_sync(0xffffffffu, inv, head_of(v));
+        if (has)
+          reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(prm.out) + row * D)[v * 32 + lane] =
+              make_uint2(E::pack2(acc[v].x * o, acc[v].y * o), E::pack2(acc[v].z * o, acc[v].w * o));
+      }
+      if (lane < G && prm.lse)
+        prm.lse[row + lane] = sum == 0.f ? -INFINITY : (top + lg2(sum)) * kLn2;
     }
   } else {
     // ------------------------------------------------------ softmax + epilogue
     const int t = threadIdx.x;                          // key of the tile, then dimension
     const uint32_t lane_off = uint32_t(warp * 32) << 16;
-    const float scale0 = prm.sm_scale * kLog2e;
     // The four warps meet at named barriers, so none of them leaves alone: after
     // a wait that ran out (`ok` false; no wait waits any more) a warp goes on,
     // and the vote at the next item's start ends all four.
@@ -451,97 +557,15 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
         abort_flag = 1;
       }
     };
-    auto take = [&](int n) {
-      int it = -1;
-      if (ok && lane == 0) {
-        ok = item_at(n, it);
-        item_done(n);
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0) != 0;
-      return __shfl_sync(0xffffffffu, it, 0);
-    };
-    // q: warp i loads heads i and i + 4, DPL elements per lane
-    using QWord = typename std::conditional<C::DPL == 8, uint4,
-                                            typename std::conditional<C::DPL == 4, uint2, uint32_t>::type>::type;
-    QWord qw[C::HPW];
-    auto load_q = [&](const WorkItem& w) {
-#pragma unroll
-      for (int x = 0; x < C::HPW; ++x)
-        if (warp + 4 * x < G)
-          qw[x] = *reinterpret_cast<const QWord*>(
-              reinterpret_cast<const uint16_t*>(prm.q) +
-              (size_t(w.q_row) * prm.num_qo_heads + w.head * G + warp + 4 * x) * D + lane * C::DPL);
-    };
-    // ... and writes them as e4m3 terms into the q buffer of item n
-    auto write_q = [&](int n) {
-#pragma unroll
-      for (int y = 0; y < C::HPW; ++y) {
-        const int h = warp + 4 * y;
-        if (h >= G) break;
-        float x[C::DPL];
-        if constexpr (C::DPL == 8) {
-          unpack8<E>(qw[y], x);
-        } else if constexpr (C::DPL == 4) {
-          x[0] = E::lo(qw[y].x); x[1] = E::hi(qw[y].x); x[2] = E::lo(qw[y].y); x[3] = E::hi(qw[y].y);
-        } else {
-          x[0] = E::lo(qw[y]); x[1] = E::hi(qw[y]);
-        }
-        float a = 0.f;
-#pragma unroll
-        for (int e = 0; e < C::DPL; ++e) {
-          const float b = fabsf(x[e]);
-          a = b < INFINITY ? fmaxf(a, b) : a;
-        }
-        a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
-        const uint32_t u = __float_as_uint(a);
-        // the smallest k >= -100 with a <= 448 * 2^k
-        const int k = max(int(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
-        const float inv = pow2i(-k);
-#pragma unroll
-        for (int e = 0; e < C::DPL; ++e)   // (the conversion saturates infinities: NaN instead)
-          x[e] = fabsf(x[e]) < INFINITY ? x[e] * inv : __uint_as_float(0x7fc00000u);
-        const int off = lane * C::DPL, slice = off / 128, byte = off % C::ROWB;
-#pragma unroll
-        for (int tm = 0; tm < C::TERMS; ++tm) {
-          const int row = tm * G + h;
-          const int sw = C::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
-          uint8_t* dst = gen + C::OFF_Q + (n & 1) * C::QBYTES + slice * C::N * C::ROWB +
-                         row * C::ROWB + (((byte >> 4) ^ sw) << 4) + (byte & 15);
-          uint32_t code[(C::DPL + 3) / 4];
-#pragma unroll
-          for (int e = 0; e < C::DPL; e += 2) {
-            const uint32_t c = E4m3::from_f32x2(x[e], x[e + 1]);
-            const uint32_t f = E4m3::to_f16x2(c);
-            x[e] = (x[e] - Fp16::lo(f)) * 16.f;
-            x[e + 1] = (x[e + 1] - Fp16::hi(f)) * 16.f;
-            if (e % 4 == 0) code[e / 4] = c;
-            else code[e / 4] |= c << 16;
-          }
-          if constexpr (C::DPL == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
-          else if constexpr (C::DPL == 4) *reinterpret_cast<uint32_t*>(dst) = code[0];
-          else *reinterpret_cast<uint16_t*>(dst) = uint16_t(code[0]);
-        }
-        if (lane == 0) q_unit[n & 1][h] = scale0 * pow2i(k);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.q_full[n & 1]));
-    };
-    int it = take(0), merges = 0;
-    WorkItem w;
-    if (it >= 0) {
-      w = prm.items[it];
-      load_q(w);
-      write_q(0);
-    }
+    int merges = 0;
     for (int n = 0;; ++n) {
-      // (also: q_unit of every head is there)
+      WorkItem w;
+      w.req = -1;
+      if (ok) ok = take_item_warp(n, w);
       ok = !named_bar_or(1, 128, !ok);
-      if (!ok || it < 0) break;
-      const int it_next = take(n + 1);
-      WorkItem wn;
-      if (it_next >= 0) wn = prm.items[it_next];
+      if (!ok || w.req < 0) break;
       const int nt = tiles_of(w), lead = lead_of(w);
+      wait(bars.q_full[n & 1], (n >> 1) & 1);
       float unit[G], m[G], l[G];
 #pragma unroll
       for (int h = 0; h < G; ++h) {
@@ -549,8 +573,9 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
         m[h] = -INFINITY;
         l[h] = 0.f;
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.q_empty[n & 1]));
       float ref = 1.f;   // r
-      if (nt == 0 && it_next >= 0) load_q(wn);
       for (int j = 0; j < nt; ++j, ++g) {
         const int st = g % C::NST;
         // this key's page scales
@@ -659,23 +684,36 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
 #pragma unroll
             for (int b = 0; b < C::DB; ++b)
 #pragma unroll
-              for (int c = 0; c < C::ROWB / 16; ++c)
-                st_shared_zero16(base + st * C::STAGE + C::KBYTES + (b * C::T + t) * C::ROWB + c * 16);
+              for (int c = 0; c < C::ROWB / 16; ++c)   // (spread over the banks)
+                st_shared_zero16(base + st * C::STAGE + C::KBYTES + (b * C::T + t) * C::ROWB +
+                                 ((c + lane) % (C::ROWB / 16)) * 16);
           }
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[g & 1]));
-        if (j == 0 && it_next >= 0) load_q(wn);   // (its work item is there by now)
       }
-      if (it_next >= 0) write_q(n + 1);
       // ---- epilogue: the sums of the four warps' keys
+      {
+        // halving the heads a lane adds up with each exchange: after log2 G of
+        // them a lane has one head, in the bits of its number from 16 down
+        float x[G];
 #pragma unroll
-      for (int h = 0; h < G; ++h) {
+        for (int h = 0; h < G; ++h) x[h] = l[h];
+        int head = 0, d = 16;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
-        if (lane == 0) sum_sh[warp][h] = l[h];
+        for (int c = G / 2; c > 0; c /= 2, d >>= 1) {
+          const bool up = lane & d;
+#pragma unroll
+          for (int h = 0; h < c; ++h)
+            x[h] = (up ? x[h + c] : x[h]) + __shfl_xor_sync(0xffffffffu, up ? x[h] : x[h + c], d);
+          head += up ? c : 0;
+        }
+#pragma unroll
+        for (int e = 16; e > 0; e >>= 1)
+          if (e <= 16 / G) x[0] += __shfl_xor_sync(0xffffffffu, x[0], e);
+        if ((lane & (32 / G - 1)) == 0) sum_sh[warp][head] = x[0];
       }
       sync4();
       float f[G];
@@ -683,7 +721,7 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
       for (int h = 0; h < G; ++h) {
         l[h] = (sum_sh[0][h] + sum_sh[1][h]) + (sum_sh[2][h] + sum_sh[3][h]);
         // (a NaN sum, from a NaN in q or in the cache, stays one)
-        f[h] = l[h] == 0.f ? 0.f : prm.v_scale * ref / (kWeightUnit * l[h]);
+        f[h] = l[h] == 0.f ? 0.f : __fdividef(prm.v_scale * ref, kWeightUnit * l[h]);
       }
       const bool split = w.slot >= 0;
       const size_t orow = size_t(split ? w.slot : w.q_row) * prm.num_qo_heads + w.head * G;
@@ -730,8 +768,6 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
         if (lane == 0) mbar_arrive(smem_u32(&bars.m_full[e]));
         ++merges;
       }
-      w = wn;
-      it = it_next;
     }
     // no more merges
     {
