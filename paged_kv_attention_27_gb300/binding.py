@@ -144,21 +144,38 @@ def _check(status: int, where: str):
 
 def _ptr(x):
     """Device/host address of a tensor, numpy array, int, or None."""
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        pass
     if x is None:
         return None
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if isinstance(x, np.ndarray):
         return x.ctypes.data
     raise TypeError(f"cannot take the address of {type(x)}")
 
 
+_raw_stream = None   # the current stream's address, from the device's number
+
+
+def _current_stream():
+    """Address of torch's current stream on the current device. (Building the
+    Stream object takes 3 us, more than the library's own part of a small
+    call; torch's raw accessor gives the address alone.)"""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+        torch.cuda.current_stream()   # (initialises CUDA, or raises without a device)
+    return _raw_stream(torch.cuda.current_device())
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
     return stream

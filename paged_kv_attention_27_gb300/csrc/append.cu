@@ -17,6 +17,8 @@
 // where they are 16 runs, spreads each over up to 2 * num_kv_heads blocks.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "elem.cuh"
 #include "kernels.cuh"
 
@@ -45,10 +47,10 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8]) {
                     E4m3::from_f32x2(f[4], f[5]) | (E4m3::from_f32x2(f[6], f[7]) << 16));
 }
 
-// Whether row t begins a run: it does not continue row t - 1 within a page.
-__device__ __forceinline__ bool run_start(const int64_t* slots, int t, int P) {
-  const int64_t s = slots[t];
-  return s >= 0 && (t == 0 || s % P == 0 || slots[t - 1] + 1 != s);
+// Registers: a run of up to 8 passes leaves room for four blocks per SM.
+template <int D, int P>
+constexpr int min_blocks() {
+  return P * D / 256 <= 8 ? 4 : P * D / 256 <= 16 ? 2 : 1;
 }
 
 // One run, one kv head, K or V: rows [t, t + n) of the call into page `page`
@@ -60,31 +62,48 @@ __device__ __forceinline__ void append_run(const uint16_t* src, int64_t row_stri
   constexpr int LPR = D / 8;            // lanes per row, 8 elements each
   constexpr int RPP = 32 / LPR;         // rows per pass
   constexpr int PASSES = P / RPP;       // a whole page
+  constexpr int HELD = PASSES < 16 ? PASSES : 16;   // in registers; the rest is read twice
   const int row0 = lane / LPR, col = (lane % LPR) * 8;
-  // pass i holds row i * RPP + row0 of the run
-  uint4 x[PASSES];
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
+  // pass i has row i * RPP + row0 of the run
+  auto load = [&](int i) {
     const int r = i * RPP + row0;
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < n) x[i] = *reinterpret_cast<const uint4*>(src + r * row_stride + col);
-  }
+    return r < n ? *reinterpret_cast<const uint4*>(src + r * row_stride + col)
+                 : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint4 x[HELD];
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) x[i] = load(i);
   const float old = first > 0 ? *scale : 0.f;
-  float m = 0.f;
-  bool odd = false;   // a NaN, an infinity, or a scale that is no power of two
+  // |x| of bf16 and fp16 orders as its 15 bits: the largest of all elements,
+  // two at a time
+  constexpr uint32_t kInf = std::is_same<E, Bf16>::value ? 0x7f80u : 0x7c00u;
+  uint32_t top2 = 0u;
+  auto largest = [&](const uint4& y) {
+    top2 = __vmaxu2(top2, y.x & 0x7fff7fffu);
+    top2 = __vmaxu2(top2, y.y & 0x7fff7fffu);
+    top2 = __vmaxu2(top2, y.z & 0x7fff7fffu);
+    top2 = __vmaxu2(top2, y.w & 0x7fff7fffu);
+  };
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    float f[8];
-    unpack8<E>(x[i], f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float a = fabsf(f[e]);
-      const bool fine = a < INFINITY;
-      odd |= !fine;
-      m = fine ? fmaxf(m, a) : m;
-    }
+  for (int i = 0; i < HELD; ++i) largest(x[i]);
+  if (PASSES > HELD && n > HELD * RPP) {
+#pragma unroll 4
+    for (int i = HELD; i < PASSES; ++i) largest(load(i));
   }
-  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  const uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 >> 16, top2 & 0xffffu));
+  float m = E::lo(top);
+  bool odd = top >= kInf;   // a NaN, an infinity, or a scale that is no power of two
+  if (odd) {                // (rare) the largest of the finite ones
+    m = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < PASSES; ++i) {
+      float f[8];
+      unpack8<E>(load(i), f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fabsf(f[e]) < INFINITY ? fmaxf(m, fabsf(f[e])) : m;
+    }
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  }
   const int k = scale_exponent(m);
   float s = pow2(k), inv = pow2(-k);
   if (first > 0) {
@@ -106,12 +125,11 @@ __device__ __forceinline__ void append_run(const uint16_t* src, int64_t row_stri
     }
   }
   if (lane == 0 && !(first > 0 && s == old)) *scale = s;
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
+  auto store = [&](int i, const uint4& y) {
     const int r = i * RPP + row0;
-    if (r >= n) continue;
+    if (r >= n) return;
     float f[8];
-    unpack8<E>(x[i], f);
+    unpack8<E>(y, f);
     if (!odd) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] *= inv;
@@ -121,34 +139,46 @@ __device__ __forceinline__ void append_run(const uint16_t* src, int64_t row_stri
         f[e] = fabsf(f[e]) < INFINITY ? f[e] / s : __uint_as_float(0x7fc00000u);
     }
     *reinterpret_cast<uint2*>(dst + (first + r) * slot_stride + col) = codes8(f);
+  };
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) store(i, x[i]);
+  if (PASSES > HELD && n > HELD * RPP) {
+#pragma unroll 4
+    for (int i = HELD; i < PASSES; ++i) store(i, load(i));
   }
 }
 
 template <int D, class E, int P>
-__global__ void __launch_bounds__(32 * kWarps) append_scaled_kernel(AppendParams p) {
+__global__ void __launch_bounds__(32 * kWarps, min_blocks<D, P>()) append_scaled_kernel(AppendParams p) {
   __shared__ int start_sh[kRows], n_sh[kRows], count_sh;
+  __shared__ int64_t slot_sh[kRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t0 = blockIdx.x * kRows;
   if (warp == 0) {
-    const int t = t0 + lane;
-    const bool in = lane < kRows && t < p.num_tokens;
-    const int64_t slot = in ? p.slot_map[t] : -1;
-    bool start = in && run_start(p.slot_map, t, P);
-    if (in && slot >= int64_t(p.num_pages) * P) {
-      atomicOr(p.err, kErrBounds);
-      start = false;
+    // bit i of `more`: row t0 + i continues row t0 + i - 1 within a page (64
+    // rows: this block's and the longest run that can follow from its last one)
+    static_assert(kRows + 32 <= 64, "");
+    int64_t slot[2];
+    uint64_t more = 0;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int t = t0 + 32 * w + lane;
+      slot[w] = t < p.num_tokens ? p.slot_map[t] : -1;
+      int64_t before = __shfl_up_sync(0xffffffffu, slot[w], 1);
+      const int64_t last = __shfl_sync(0xffffffffu, slot[0], 31);
+      if (lane == 0) before = w == 1 ? last : t > 0 ? p.slot_map[t - 1] : -2;
+      const bool on = slot[w] >= 0 && slot[w] % P != 0 && before + 1 == slot[w];
+      more |= uint64_t(__ballot_sync(0xffffffffu, on)) << (32 * w);
     }
-    int n = 0;
-    if (start) {
-      const int most = min(P - int(slot % P), p.num_tokens - t);
-      n = 1;
-      while (n < most && p.slot_map[t + n] == slot + n) ++n;
-    }
+    const bool in = lane < kRows && slot[0] >= 0 && slot[0] < int64_t(p.num_pages) * P;
+    if (lane < kRows && slot[0] >= int64_t(p.num_pages) * P) atomicOr(p.err, kErrBounds);
+    const bool start = in && !((more >> lane) & 1u);
     const uint32_t starts = __ballot_sync(0xffffffffu, start);
     if (start) {
       const int at = __popc(starts & ((1u << lane) - 1u));
-      start_sh[at] = t;
-      n_sh[at] = n;
+      start_sh[at] = t0 + lane;
+      slot_sh[at] = slot[0];
+      n_sh[at] = __ffsll(~(more >> (lane + 1)));   // (bits past the last one are clear)
     }
     if (lane == 0) count_sh = __popc(starts);
   }
@@ -161,7 +191,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_scaled_kernel(AppendParams
     const bool is_v = hk >= p.num_kv_heads;
     const int h = is_v ? hk - p.num_kv_heads : hk;
     const int t = start_sh[run], n = n_sh[run];
-    const int64_t slot = p.slot_map[t];
+    const int64_t slot = slot_sh[run];
     const int64_t page = slot / P;
     const int first = int(slot - page * P);
     const uint16_t* src = reinterpret_cast<const uint16_t*>(is_v ? p.v_new : p.k_new) +
