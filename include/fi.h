@@ -504,7 +504,8 @@ fi_status fi_merge_states(const float* v, const float* s, int32_t n, int32_t S, 
  *   kv_len           device int32 [max_requests]; kv_len_out the same, and
  *                    may be kv_len itself.
  *   block_table      device int32 [max_requests][max_pages], in and out.
- *   free_ring        device int32 [ring_capacity], in and out.
+ *   free_ring        device int32 [ring_capacity], in and out; ring_capacity,
+ *                    page_capacity and token_capacity at most 2^30.
  *   ring_state       device int32 {head, count}; ring_state_out the same,
  *                    and may be ring_state itself.
  *   page_indices     device int32 [page_capacity].

@@ -222,7 +222,16 @@ fi_status host_steps_ready(HostSteps& h) {
 // or not at all (the host-buffer call uploads it with the page table).
 enum class Upload { kStaged, kStatic, kDone };
 
+// A small image of a page-scaled plan goes as a kernel parameter: 4 us less of
+// host time than the staging copy with its events, and the launch behind it
+// waits for a kernel of 1 us instead of the copy engine.
 fi_status upload_image(void* dst, const fi::Plan& P, cudaStream_t stream) {
+  if (P.kv_dtype == FI_DTYPE_E4M3_PAGE && P.ws.image_end <= fi::kImageParamBytes) {
+    fi::ImageParam image;
+    fill_image(reinterpret_cast<uint8_t*>(image.words), P);
+    const cudaError_t e = fi::launch_image(image, P.ws.image_end, dst, stream);
+    return e == cudaSuccess ? FI_OK : cuda_fail(e, "work-list launch");
+  }
   return stage_and_copy(g_staging, dst, P.ws.image_end,
                         [&](uint8_t* p) { fill_image(p, P); }, stream, "work-list upload");
 }
@@ -929,7 +938,8 @@ fi_status fi_page_table_step(int32_t batch, const int32_t* slots, const int32_t*
   if (batch < 0 || batch > fi::kStepMaxBatch || max_requests < 1 ||
       max_requests > fi::kStepMaxRequests || max_pages < 1 || page_size < 1 ||
       page_size > fi::kStepMaxPageSize || ring_capacity < 1 || page_capacity < 0 ||
-      token_capacity < 0)
+      token_capacity < 0 || ring_capacity > fi::kStepMaxEntries ||
+      page_capacity > fi::kStepMaxEntries || token_capacity > fi::kStepMaxEntries)
     return FI_ERR_INVALID_ARG;
   if (batch == 0) return FI_OK;
   if (!new_len || !kv_len || !kv_len_out || !block_table || !free_ring || !ring_state ||

@@ -172,6 +172,12 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
     abort_flag = 0;
     fence_barrier_init();
   }
+  // The first item and its pages' ids: on their way during the set-up below.
+  WorkItem w0;
+  w0.req = -1;
+  int page0 = -1;
+  if (warp == 4 || warp == 7) w0 = prm.items[blockIdx.x];   // (the grid has no more CTAs than items)
+  if (warp == 4 && lane < min(ppt, w0.n_pages)) page0 = prm.page_indices[w0.page_begin + lane];
   // rows of Q that no head uses stay zero
   for (int i = threadIdx.x; i < 2 * C::QBYTES / 16; i += C::THREADS)
     st_shared_zero16(base + C::OFF_Q + i * 16);
@@ -216,12 +222,9 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
     };
     auto pages_in = [&](const WorkItem& w, int j) { return min(ppt, w.n_pages - j * ppt); };
     int g = 0;
-    WorkItem w, wn;
-    look_up(int(blockIdx.x), w);
+    WorkItem w = w0, wn;
     bool ok = publish(0, w);
-    int next_page = -1;
-    if (ok && w.req >= 0 && lane < pages_in(w, 0))
-      next_page = prm.page_indices[w.page_begin + lane];
+    int next_page = page0;
     for (int n = 0; ok && w.req >= 0; ++n) {
       const int nt = tiles_of(w);
       const int c1 = prm.layout == FI_LAYOUT_NHD ? w.head : 0;
@@ -380,8 +383,8 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
     const int h = lane / LPH, off = lane % LPH * EPL;
     bool ok = true;
     for (int n = 0;; ++n) {
-      WorkItem w;
-      ok = take_item_warp(n, w);
+      WorkItem w = w0;   // (item 0 is read before it is published)
+      if (n > 0) ok = take_item_warp(n, w);
       if (!ok || w.req < 0) break;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
           reinterpret_cast<const uint16_t*>(prm.q) +
@@ -397,6 +400,7 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
 #pragma unroll
         for (int e = 0; e < WORDS; ++e) u[e] = src[e];
       }
+      if (n == 0) ok = take_item_warp(0, w);
       if (n >= 2) ok = mbar_sleep_warp(smem_u32(&bars.q_empty[n & 1]), ((n - 2) >> 1) & 1, limit,
                                        &abort_flag);
       if (!ok) break;

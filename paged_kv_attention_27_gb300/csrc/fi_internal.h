@@ -65,6 +65,7 @@ constexpr size_t kStepTicketOffset = 64;
 constexpr int32_t kStepMaxBatch = 8192;
 constexpr int32_t kStepMaxRequests = 262144;
 constexpr int32_t kStepMaxPageSize = 1024;
+constexpr int32_t kStepMaxEntries = 1 << 30;   // of the ring, page_indices, slot_map
 
 inline int decode_tile_tokens(int head_dim) { return 8192 / head_dim; }  // 32 KB of K+V
 // The kernels over a page-scaled FP8 cache: tokens per tile of the decode

@@ -141,6 +141,14 @@ cudaError_t launch_prefill_page8(int head_dim, int dtype, const void* q,
                                  const PrefillParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_merge(const MergeParams& p, int n_rows, cudaStream_t stream);
 
+// A small work-list image as a kernel parameter (merge.cu): one launch in
+// place of a staging copy. `bytes` is a multiple of 16, at most the capacity.
+constexpr size_t kImageParamBytes = 3840;
+struct ImageParam {
+  uint32_t words[kImageParamBytes / 4];
+};
+cudaError_t launch_image(const ImageParam& image, size_t bytes, void* dst, cudaStream_t stream);
+
 // fi_page_table_step (page_step.cu): the arguments of the call, and the step
 // workspace's error word and ticket.
 struct PageStepParams {

@@ -58,7 +58,23 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeParams p) {
   }
 }
 
+// One 16-byte piece per thread from the parameter to the workspace.
+__global__ void __launch_bounds__(kImageParamBytes / 16)
+image_kernel(const __grid_constant__ ImageParam image, uint4* dst, int pieces) {
+  const int i = threadIdx.x;
+  if (i < pieces)
+    dst[i] = make_uint4(image.words[4 * i], image.words[4 * i + 1], image.words[4 * i + 2],
+                        image.words[4 * i + 3]);
+}
+
 }  // namespace
+
+cudaError_t launch_image(const ImageParam& image, size_t bytes, void* dst, cudaStream_t stream) {
+  const int pieces = int(bytes / 16);
+  if (pieces <= 0) return cudaSuccess;
+  image_kernel<<<1, (pieces + 31) / 32 * 32, 0, stream>>>(image, static_cast<uint4*>(dst), pieces);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_merge(const MergeParams& p, int n_rows, cudaStream_t stream) {
   if (n_rows <= 0 || p.H <= 0) return cudaSuccess;

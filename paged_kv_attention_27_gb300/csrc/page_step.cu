@@ -56,16 +56,21 @@ __device__ __forceinline__ Sums warp_scan(Sums a, int lane) {
   return a;
 }
 
-// The row whose range of `ends` (non-decreasing inclusive sums) holds item i,
-// i < ends[n - 1].
-__device__ __forceinline__ int owner(const int32_t* ends, int n, int32_t i) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (ends[mid] > i) hi = mid;
-    else lo = mid + 1;
+// The rows whose ranges of `ends` (non-decreasing inclusive sums) hold the
+// items i[c], i[c] < ends[n - 1]: the number of sums at or below each, by
+// bisection, C searches side by side. `first` is the largest power of two <= n.
+template <int C>
+__device__ __forceinline__ void owners(const int32_t* ends, int n, int first, const int32_t (&i)[C],
+                                       int (&r)[C]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) r[c] = 0;
+  for (int s = first; s > 0; s >>= 1) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (r[c] + s <= n && ends[r[c] + s - 1] <= i[c]) r[c] += s;
   }
-  return lo;
+#pragma unroll
+  for (int c = 0; c < C; ++c) r[c] = min(r[c], n - 1);   // (items behind the last one)
 }
 
 template <bool CLUSTER>
@@ -182,40 +187,77 @@ __global__ void __launch_bounds__(kThreads) page_step_kernel(PageStepParams p) {
   auto row_of = [&](int slot) { return p.block_table + (long long)slot * p.max_pages; };
   const int gtid = blockIdx.x * kThreads + tid, gsize = gridDim.x * kThreads;
   const int n_rows = ok ? int(total.rows) : 0;
+  const int first = 1 << (31 - __clz(p.batch));
   if (ok) {
-#pragma unroll 4
-    for (int i = gtid; i < int(total.has); i += gsize) {
-      const int r = owner(has_end, p.batch, i);
-      const int j = i - (r > 0 ? has_end[r - 1] : 0);
-      const int had = (old_sh[r] + P - 1) / P;
-      int32_t* entry = row_of(slot_sh[r]) + j;
-      const bool fresh = j >= had;
-      const int page =
-          fresh ? *ring_at(uint32_t((r > 0 ? take_end[r - 1] : 0) + j - had)) : *entry;
-      if (fresh) *entry = page;
-      p.page_indices[i] = page;
+    constexpr int C = 4;
+    for (int i0 = gtid; i0 < int(total.has); i0 += C * gsize) {
+      int32_t i[C];
+      int r[C], page[C];
+      int32_t* entry[C];
+      bool fresh[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) i[c] = i0 + c * gsize;
+      owners(has_end, p.batch, first, i, r);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int j = i[c] - (r[c] > 0 ? has_end[r[c] - 1] : 0);
+        const int had = (old_sh[r[c]] + P - 1) / P;
+        entry[c] = row_of(slot_sh[r[c]]) + j;
+        fresh[c] = j >= had;
+        page[c] = -1;
+        if (i[c] < int(total.has))
+          page[c] = fresh[c] ? *ring_at(uint32_t((r[c] > 0 ? take_end[r[c] - 1] : 0) + j - had))
+                             : *entry[c];
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (i[c] >= int(total.has)) continue;
+        if (fresh[c]) *entry[c] = page[c];
+        p.page_indices[i[c]] = page[c];
+      }
     }
-    for (int i = gtid; i < int(total.give); i += gsize) {
-      const int r = owner(give_end, p.batch, i);
-      const int has = has_end[r] - (r > 0 ? has_end[r - 1] : 0);
-      const int j = has + i - (r > 0 ? give_end[r - 1] : 0);
-      *ring_at(uint32_t(count) + uint32_t(i)) = row_of(slot_sh[r])[j];
+    for (int i0 = gtid; i0 < int(total.give); i0 += gsize) {
+      const int32_t i[1] = {i0};
+      int r[1];
+      owners(give_end, p.batch, first, i, r);
+      const int x = r[0];
+      const int has = has_end[x] - (x > 0 ? has_end[x - 1] : 0);
+      const int j = has + i0 - (x > 0 ? give_end[x - 1] : 0);
+      *ring_at(uint32_t(count) + uint32_t(i0)) = row_of(slot_sh[x])[j];
     }
   }
-#pragma unroll 2
-  for (int t = gtid; t < p.token_capacity; t += gsize) {
-    long long where = -1;
-    int pos = 0;
-    if (t < n_rows) {
-      const int r = owner(row_end, p.batch, t);
-      pos = old_sh[r] + t - (r > 0 ? row_end[r - 1] : 0);
-      const int j = pos / P, had = (old_sh[r] + P - 1) / P;
-      const int page = j < had ? row_of(slot_sh[r])[j]
-                               : *ring_at(uint32_t((r > 0 ? take_end[r - 1] : 0) + j - had));
-      where = (long long)page * P + pos % P;
+  {
+    constexpr int C = 2;
+    for (int t0 = gtid; t0 < p.token_capacity; t0 += C * gsize) {
+      int32_t t[C];
+      int r[C], pos[C];
+      long long where[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        t[c] = t0 + c * gsize;
+        pos[c] = 0;
+        where[c] = -1;
+      }
+      if (t0 < n_rows) {
+        owners(row_end, p.batch, first, t, r);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          if (t[c] >= n_rows) continue;
+          const int x = r[c];
+          pos[c] = old_sh[x] + t[c] - (x > 0 ? row_end[x - 1] : 0);
+          const int j = pos[c] / P, had = (old_sh[x] + P - 1) / P;
+          const int page = j < had ? row_of(slot_sh[x])[j]
+                                   : *ring_at(uint32_t((x > 0 ? take_end[x - 1] : 0) + j - had));
+          where[c] = (long long)page * P + pos[c] % P;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (t[c] >= p.token_capacity) continue;
+        p.slot_map[t[c]] = where[c];
+        if (p.positions) p.positions[t[c]] = pos[c];
+      }
     }
-    p.slot_map[t] = where;
-    if (p.positions) p.positions[t] = pos;
   }
 
   // every block has read the old lengths and ring state: now the new ones

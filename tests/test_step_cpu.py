@@ -52,6 +52,13 @@ def test_page_table_step_refusals(bad):
     assert _status(lambda **k: B.fi_page_table_step(**args, **k), ()) == B.FI_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("name", ["ring_capacity", "page_capacity", "token_capacity"])
+def test_page_table_step_capacity_limit(name):
+    _no_gpu()
+    for n, status in ((2 ** 30, B.FI_ERR_NO_DEVICE), (2 ** 30 + 1, B.FI_ERR_INVALID_ARG)):
+        assert _status(lambda **k: B.fi_page_table_step(**{**STEP, name: n}, **k), ()) == status
+
+
 def test_page_table_step_accepts_what_it_documents():
     _no_gpu()
     call = lambda **kw: _status(lambda **k: B.fi_page_table_step(**{**STEP, **kw}, **k), ())
