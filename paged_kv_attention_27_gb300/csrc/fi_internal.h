@@ -71,6 +71,7 @@ inline int decode_tile_tokens(int head_dim) { return 8192 / head_dim; }  // 32 K
 // The kernels over a page-scaled FP8 cache: tokens per tile of the decode
 // kernel; M rows (query rows x the g heads of a kv head) of a prefill item.
 constexpr int kPage8DecodeTile = 128;
+inline int page8_decode_ctas(int head_dim) { return head_dim <= 128 ? 2 : 1; }   // per SM
 inline int page8_prefill_rows(int head_dim) { return head_dim <= 128 ? 256 : 128; }
 // A batch with both decode rows and multi-row (chunked prefill) requests runs
 // as one persistent launch of the mixed kernel for these shapes (q/out and

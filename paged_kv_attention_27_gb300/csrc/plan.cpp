@@ -178,7 +178,14 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
     // chunks below 512 tokens (per-CTA setup would dominate). (The mixed
     // kernel measured slowest with finer chunks: 1.745 ms per call at this
     // target, 1.770 at twice it, 1.848 at four times.)
-    const int64_t target = int64_t(num_sms) * 2 * 4;
+    // Over a page-scaled cache an item's start and end cost about as much as
+    // two of its (larger) tiles: half as many items, and where a resident CTA's
+    // share is a dozen tiles or less, one item each. (70B-shaped batch 164 us at
+    // eight items per SM, 158 at four, 169 at two; one request of 30K keys 53 us
+    // in chunks of 512, 41 in one wave.)
+    const int64_t slots = int64_t(num_sms) * page8_decode_ctas(head_dim);
+    const int64_t target = !page8 ? int64_t(num_sms) * 2 * 4
+                                  : dec_tiles <= 12 * slots ? slots : int64_t(num_sms) * 4;
     const int64_t min_chunk_tiles = std::max<int64_t>(1, 512 / tile);
     const int64_t chunk_tiles = std::max(min_chunk_tiles, ceil_div(dec_tiles, target));
     const int64_t chunk = chunk_tiles * tile;  // a multiple of the page size

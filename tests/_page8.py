@@ -10,14 +10,26 @@ the value, eps / 2; a = sum p |v| over the row's keys, p normalised):
                                 itself, three (fp16) by 2^-12; 16-bit weights
                                 (prefill) by at most 2^-8 (bf16) and 2^-11
   + n u vmax pmax               weights so small that their last term is
-                                subnormal: at most u of the largest weight,
-                                2^-20 (two terms), 2^-24 (three, or fp16)
+                                subnormal: at most u of the largest weight.
+                                Decode stores a weight w <= 2^4 as terms of
+                                16 w, the second times 16, the third times 256:
+                                half of E4M3's step of 2^-9 is 2^-10 / 256 =
+                                2^-18 of a weight of 1 (two terms) or 2^-22
+                                (three); the running maximum is within a factor
+                                of 2^4 of the largest weight, which is >= 1 when
+                                it is set. Prefill's fp16 weights: 2^-25.
   + 2 d (a + |o|)               d: the error of the scores (below), which is a
                                 relative error of each weight and of their sum
 The fp32 sums of a score's head_dim products (times the fp32 roundings of the
 scales) are off by at most (head_dim + 8) 2^-24 of sum |q k|; the exponentials
 of ex2.approx by 2^-22: d = (head_dim + 8) 2^-24 max sum |q k| sm_scale +
-2^-20. The bound on lse is d + 2^-22 |lse|."""
+2^-20. To d also belong q's elements that E4M3's finest step rounds: q enters
+as terms of x = q times a power of two with the row's largest |x| in 224..448;
+prefill's terms are exact down to the step 2^-9, so an element of bf16 (8 bits)
+is exact from |x| = 2^-2 on, of fp16 (11 bits, three terms) from 2 on, and one
+below is off by at most 2^-10; decode's last term is scaled by 16 (256), so
+its elements are exact from 2^-6 (2^-7) on and off by at most 2^-14 (2^-18):
++ sm_scale max_t sum_e off_e |k_te|. The bound on lse is d + 2^-22 |lse|."""
 import numpy as np
 
 from . import _step
@@ -163,7 +175,12 @@ def reference(b, requests=None, k_scale=1.0, v_scale=1.0):
             a[r0:r0 + m, h] = p @ np.abs(vv)
             # weights enter times their page's value scale: p |v| at its largest
             tiny[r0:r0 + m, h] = n * (p * np.abs(vv).max(axis=1)[None]).max(axis=1)
-            ds[r0:r0 + m, h] = ((b.d + 8) * 2.0 ** -24 * b.sm_scale *
+            fine, off = {(True, "bf16"): (-6, -14), (True, "fp16"): (-7, -18),
+                         (False, "bf16"): (-2, -10), (False, "fp16"): (1, -10)}[b.decode, b.dtype]
+            unit = np.abs(qq).max(axis=1, keepdims=True) / 224       # at least x's unit
+            off_q = np.where(np.abs(qq) < unit * 2.0 ** fine, unit * 2.0 ** off, 0)
+            ds[r0:r0 + m, h] = (b.sm_scale * np.where(vis, off_q @ np.abs(kk).T, 0).max(axis=1) +
+                                (b.d + 8) * 2.0 ** -24 * b.sm_scale *
                                 np.where(vis, np.abs(qq) @ np.abs(kk).T, 0).max(axis=1) + 2.0 ** -20)
     return out, lse, a, tiny, ds
 
@@ -173,7 +190,7 @@ def compare(b, out, lse, ref, rows=None, what=""):
     ro, rl, a, tiny, ds = ref
     if rows is not None:
         o, l, ro, rl, a, tiny, ds = [x[rows] for x in (o, l, ro, rl, a, tiny, ds)]
-    h, r, u = (2.0 ** -8, 2.0 ** -8, 2.0 ** -20) if b.dtype == "bf16" else (2.0 ** -11, 2.0 ** -11, 2.0 ** -24)
+    h, r, u = (2.0 ** -8, 2.0 ** -8, 2.0 ** -18) if b.dtype == "bf16" else (2.0 ** -11, 2.0 ** -11, 2.0 ** -22)
     bound = h * np.abs(ro) + r * a + u * tiny[..., None] + 2 * ds[..., None] * (a + np.abs(ro))
     assert np.all(np.isfinite(o)), f"{what}: non-finite output"
     err = np.abs(o - ro)
