@@ -593,8 +593,8 @@ fi_status run_paged(fi_plan_t plan, bool prefill_call, const void* q, const int3
       dstream = side.stream;
     }
     if (!P.prefill_items.empty()) {
-      e = page8 ? fi::launch_prefill_page8(P.head_dim, P.dtype, q, kmap, vmap, pp, P.num_sms,
-                                           stream)
+      e = page8 ? fi::launch_prefill_page8(P.head_dim, P.dtype, P.prefill_solo, q, kmap, vmap, pp,
+                                           P.num_sms, stream)
                 : fi::launch_prefill(P.head_dim, P.dtype, qmap, kmap, vmap, pp, P.num_sms, stream);
       if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
     }

@@ -126,6 +126,8 @@ struct Plan {
   std::vector<WorkItem> prefix_items;
   std::vector<int32_t> prefix_tables;
   int32_t num_prefix_groups = 0;
+  // page-scaled prefill: much of the work is in items of one M tile
+  bool prefill_solo = false;
   int32_t chunk_tokens = 0;
   int32_t num_split = 0;
   int32_t num_slots = 0;

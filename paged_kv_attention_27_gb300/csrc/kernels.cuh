@@ -136,7 +136,9 @@ cudaError_t launch_decode(int head_dim, int group, int dtype, int kv_dtype, cons
 cudaError_t launch_decode_page8(int head_dim, int group, int dtype, const CUtensorMap& km,
                                 const CUtensorMap& vm, const DecodeParams& p, int n_items,
                                 int num_sms, cudaStream_t stream);
-cudaError_t launch_prefill_page8(int head_dim, int dtype, const void* q,
+// solo: items whose rows fill one of the two M tiles share it between both
+// streams (Plan::prefill_solo)
+cudaError_t launch_prefill_page8(int head_dim, int dtype, bool solo, const void* q,
                                  const CUtensorMap& km, const CUtensorMap& vm,
                                  const PrefillParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_merge(const MergeParams& p, int n_rows, cudaStream_t stream);

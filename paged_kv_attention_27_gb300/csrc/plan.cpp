@@ -330,6 +330,17 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
     return x.b != y.b ? x.b < y.b : x.qt < y.qt;
   });
 
+  if (page8 && head_dim <= 128) {
+    // work (keys) in items whose rows fill one M tile (128 / g rows)
+    int64_t one = 0, all = 0;
+    for (const Tile& t : tiles) {
+      const int64_t rows = std::min<int64_t>(tile_rows, qo_len[t.b] - int64_t(t.qt) * tile_rows);
+      all += t.len;
+      if (rows * g <= kPrefillTileM) one += t.len;
+    }
+    p.prefill_solo = one * 8 > all;
+  }
+
   // ---- KV split of prefill tiles when the launch has under two waves of
   //      work units (a CTA's unit: a tile with one head, or with a head pair
   //      on the two-tile kernel). Long tiles are then cut into pieces of

@@ -4,7 +4,13 @@
 // A work item is (rows of a request, kv head): rows x the g query heads of the
 // kv head fill the M rows of two 128-row tiles (one at head_dim 256), heads
 // inner, so that every K/V tile that is loaded serves all of them; a draft's
-// few rows and a long prompt run the same way.
+// few rows and a long prompt run the same way. Where the rows fill one M tile
+// only, the second stream of scores and outputs can take every other K/V tile
+// of the same rows (a tile's chain score -> softmax -> output is serial, and two
+// of them keep the SM busy); the two states are merged at the end. That is a
+// kernel of its own (SOLO): 48 drafts of 1-9 rows 158 -> 136 us, but launches
+// whose items fill both tiles 3 % slower, so the planner picks it where an
+// eighth of the work or more is in items of one M tile.
 //
 // Arithmetic: the scores' MMAs take the K codes as they arrive (kind::f8f6f4).
 // A q row, times the power of two that puts its largest element at 224..448,
@@ -109,7 +115,7 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
                : "memory");
 }
 
-template <int D, class E>
+template <int D, class E, bool SOLO>
 __global__ void __launch_bounds__(P8Cfg<D, E>::THREADS, 1)
 prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map, PrefillParams prm) {
@@ -478,7 +484,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
       // ------------------------------------------------------------- MMA issuers
       const int i = warp - C::W_MMA;
       if (lane == 0) {
-        const uint64_t qd0 = sdesc_swz(base + C::OFF_Q + i * C::Q, 16, C::ATOM, C::SWZ);
+        const uint64_t qd0 = sdesc_swz(base + C::OFF_Q, 16, C::ATOM, C::SWZ);
         const uint64_t kd0 = sdesc_swz(base + C::OFF_K, 16, C::ATOM, C::SWZ);
         const uint64_t vd0 = sdesc_sw128(base + C::OFF_V, C::N * 128, 1024);
         const uint32_t s_col = tmem + C::col_s(i), o_col = tmem + C::col_o(i);
@@ -487,7 +493,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
         };
         bool ok = true;
         int t = 0;      // tiles of earlier items
-        int mine = 0;   // of which this issuer's tile took part in
+        int mine = 0;   // of which this stream took
         for (int n = 0; ok; ++n) {
           int it = -1;
           ok = item_at(n, it);
@@ -496,25 +502,27 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
           const WorkItem w = prm.items[it];
           const int nt = tiles_of(w);
           ok = wait(bars.q_full, n & 1);
-          if (!active(w, i)) {
-            // keeps the rings going: its share of each tile's release
-            for (int j = 0; ok && j < nt; ++j, ++t) {
-              ok = wait(bars.k_full[t % C::NK], (t / C::NK) & 1);
-              if (ok) mbar_arrive(smem_u32(&bars.k_empty[t % C::NK]));
-              ok = ok && wait(bars.v_full[t & 1], (t >> 1) & 1);
-              if (ok) mbar_arrive(smem_u32(&bars.v_empty[t & 1]));
-            }
-            if (ok) mbar_arrive(smem_u32(&bars.q_empty));
-            continue;
-          }
-          for (int j = 0; ok && j < nt; ++j, ++t, ++mine) {
+          // Both M tiles have rows: each stream takes every K/V tile. One has:
+          // stream 0 does, or (SOLO) the streams share that M tile's q and take
+          // turns. (Separate loops: this thread is on the tiles' chains, and the
+          // conditions in one common loop cost 4 % of a launch.)
+          const bool both = C::TILES == 1 || active(w, 1);
+          const uint64_t qd = qd0 + (both ? uint64_t((i * C::Q) >> 4) : 0);
+          int of_item = 0;   // tiles of this item that this stream has taken
+          // another stream's tile: this one's share of its release
+          auto pass = [&] {
+            ok = wait(bars.k_full[t % C::NK], (t / C::NK) & 1);
+            if (ok) mbar_arrive(smem_u32(&bars.k_empty[t % C::NK]));
+            ok = ok && wait(bars.v_full[t & 1], (t >> 1) & 1);
+            if (ok) mbar_arrive(smem_u32(&bars.v_empty[t & 1]));
+          };
+          // a tile, once its K is there; `next`: the next tile is this stream's too
+          auto take = [&](bool last, bool next) {
             const int st = t & 1, ph = (t >> 1) & 1, ks = t % C::NK;
-            // (the K of later tiles was waited for while the previous tile's softmax ran)
-            if (j == 0) ok = wait(bars.k_full[ks], (t / C::NK) & 1);
             // S and P share columns, and the softmax rescales O after S is
             // full: the previous O += P V completes first
             if (ok && mine >= 1) ok = wait(bars.pv_done[i], (mine - 1) & 1);
-            if (!ok) break;
+            if (!ok) return;
             tc_fence_after();
             const uint64_t kd = kd0 + uint64_t((ks * C::CODES) >> 4);
 #pragma unroll
@@ -522,29 +530,49 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
 #pragma unroll
               for (int k = 0; k < D / 32; ++k) {
                 const int b = k * 32 / 128, o = k * 32 % 128;
-                tc_mma_f8_ss(s_col, qd0 + uint64_t((tm * C::QT + b * C::M * 128 + o) >> 4),
+                tc_mma_f8_ss(s_col, qd + uint64_t((tm * C::QT + b * C::M * 128 + o) >> 4),
                              kd + uint64_t((b * C::N * 128 + o) >> 4), C::IDESC_QK,
                              (tm > 0 || k > 0) ? 1u : 0u);
               }
             tc_commit(smem_u32(&bars.s_full[i]));
             tc_commit(smem_u32(&bars.k_empty[ks]));
-            if (j == nt - 1) tc_commit(smem_u32(&bars.q_empty));
-            if (j + 1 < nt) ok = wait(bars.k_full[(t + 1) % C::NK], ((t + 1) / C::NK) & 1);
+            if (last) tc_commit(smem_u32(&bars.q_empty));
+            // (the next K and this V are waited for while the softmax runs)
+            if (next) ok = wait(bars.k_full[(t + 1) % C::NK], ((t + 1) / C::NK) & 1);
             if (ok) ok = wait(bars.v_full[st], ph);
             if (ok) ok = wait(bars.p_full[i], mine & 1);
-            if (!ok) break;
+            if (!ok) return;
             tc_fence_after();
             const uint64_t vd = vd0 + uint64_t((st * C::V) >> 4);
 #pragma unroll
             for (int k = 0; k < C::N / 16; ++k)
               tc_mma_ts(o_col, s_col + k * 8, vd + uint64_t((k * 16 * 128) >> 4), C::IDESC_PV,
-                        (j > 0 || k > 0) ? 1u : 0u);
+                        (of_item > 0 || k > 0) ? 1u : 0u);
             tc_commit(smem_u32(&bars.v_empty[st]));
             tc_commit(smem_u32(&bars.pv_done[i]));
+            ++mine;
+            ++of_item;
+          };
+          if (both || (!SOLO && i == 0)) {
+            if (nt > 0) ok = ok && wait(bars.k_full[t % C::NK], (t / C::NK) & 1);
+            for (int j = 0; ok && j < nt; ++j, ++t) take(j == nt - 1, j + 1 < nt);
+          } else if (!SOLO) {
+            for (int j = 0; ok && j < nt; ++j, ++t) pass();
+            if (ok && nt > 0) mbar_arrive(smem_u32(&bars.q_empty));
+          } else {
+            for (int j = 0; ok && j < nt; ++j, ++t) {
+              if ((j & 1) == i) {
+                ok = wait(bars.k_full[t % C::NK], (t / C::NK) & 1);
+                take(j == nt - 1, false);
+              } else {
+                pass();
+                if (ok && j == nt - 1) mbar_arrive(smem_u32(&bars.q_empty));
+              }
+            }
           }
           if (!ok) break;
           if (nt == 0) tc_commit(smem_u32(&bars.q_empty));
-          else tc_commit(smem_u32(&bars.o_final[i]));
+          else if (of_item > 0) tc_commit(smem_u32(&bars.o_final[i]));
         }
         if (!ok) fail();
         // every MMA issued so far completes before the TMEM is released
@@ -584,8 +612,8 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
       return buf[half ^ 1][t];
     };
     int gt = 0;                    // tiles of keys of earlier items
-    int done0 = 0, done1 = 0;      // of which each M tile took part in
-    int outs0 = 0, outs1 = 0;      // items with keys each M tile took part in
+    int done0 = 0, done1 = 0;      // of which each stream took
+    int outs0 = 0, outs1 = 0;      // items of which each stream took a tile
     for (int n = 0;; ++n) {
       int it = -1;
       if (ok) ok = take_item(n, it);
@@ -596,7 +624,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
       const int q_start = prm.qo_indptr[w.req], q_end = prm.qo_indptr[w.req + 1];
       const int np_req = prm.page_indptr[w.req + 1] - prm.page_indptr[w.req];
       const int kv_len = np_req > 0 ? (np_req - 1) * P + prm.last_page_len[w.req] : 0;
-      const int n_act = w.q_row + R < q_end ? C::TILES : 1;             // M tiles with a row
+      const bool both = C::TILES == 1 || w.q_row + R < q_end;           // every M tile has a row
       // key position of this thread's row of tile 0 (tile 1: R rows on), and
       // the keys it may see, in columns of this thread's half
       const int row0 = w.q_row + t / g;
@@ -618,21 +646,24 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
         const float4* sc = scale_sh[gt % kScaleRing] + half * C::HG;
         // (one copy of this code, for the instruction cache: unrolled over the
         // M tiles, or with a second copy for masked tiles, it was slower)
+        // (the streams that have this tile, a bit each)
+        const int act = both ? 3 : 1 << (j & 1);
 #pragma unroll 1
-        for (int i = 0; i < n_act; ++i) {
+        for (int i = 0; i < (SOLO || both ? C::TILES : 1); ++i) {
+          if (SOLO && ((act >> i) & 1) == 0) continue;
           wait(bars.s_full[i], (i == 0 ? done0++ : done1++) & 1);
           tc_fence_after();
           float unit = i == 0 ? unit0 : unit1;
           float m = i == 0 ? m0 : m1, l = i == 0 ? l0 : l1;
-          if (j == 0) {
+          if (j == 0 || (SOLO && !both && j == 1)) {
             // (the first scores are there, so q's terms and exponents are.
             // Waiting for q_full itself here would be wrong: where items have
             // one tile of keys, q_full runs on to the next item's phase while
             // this warp is still in the previous item's epilogue)
-            unit = scale0 * __uint_as_float(uint32_t(int(q_exp[n & 1][i * 128 + t]) - 1) << 23);
+            unit = scale0 * __uint_as_float(uint32_t(int(q_exp[n & 1][(!SOLO || both ? i * 128 : 0) + t]) - 1) << 23);
             if (i == 0) unit0 = unit;
             else unit1 = unit;
-            if (i == 0) ref = scale_sh[gt % kScaleRing][0].w;
+            if (j == 0) ref = scale_sh[gt % kScaleRing][0].w;
           }
           const uint32_t s_col = tmem + lane_off + C::col_s(i);
           const uint32_t o_col = tmem + lane_off + C::col_o(i) + half * (D / 2);
@@ -643,7 +674,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
             for (int c = 0; c < C::H / 32; ++c) tmem_ld32(s_col + half * C::H + c * 32, sr[c]);
             tmem_wait_ld();
             if (need_mask) {
-              const int pos = pos0 + i * R, col0 = off + j * C::N;
+              const int pos = pos0 + (!SOLO || both ? i * R : 0), col0 = off + j * C::N;
               const int hi = min(prm.causal ? pos : kv_len - 1, kv_len - 1) - col0;
               const int lo = prm.window_left >= 0 ? max(pos - prm.window_left - col0, 0) : 0;
 #pragma unroll
@@ -735,9 +766,20 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
       }
       // ---- epilogue, half of the columns per warp (a piece of a split item
       // writes the rows' fp32 states)
+      // One M tile: the streams' states are added up, with weights f0 and f1.
+      float f0 = 1.f, f1 = 0.f;
+      const bool merge2 = SOLO && !both && nt > 1;
+      if (merge2) {
+        const float m2 = fmaxf(m0, m1);
+        f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m2);
+        f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m2);
+        l0 = l0 * f0 + l1 * f1;
+        m0 = m2;
+      }
 #pragma unroll 1
-      for (int i = 0; i < n_act; ++i) {
+      for (int i = 0; i < (both ? C::TILES : 1); ++i) {
         if (nt > 0) wait(bars.o_final[i], (i == 0 ? outs0++ : outs1++) & 1);
+        if (merge2) wait(bars.o_final[1], outs1++ & 1);
         const float m = i == 0 ? m0 : m1, l = i == 0 ? l0 : l1;
         const float l_other = swap(l);
         const float sum = half == 0 ? l + l_other : l_other + l;
@@ -760,6 +802,14 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[e] = 0u;
+          }
+          if (merge2) {
+            uint32_t x[32];
+            tmem_ld32(tmem + lane_off + C::col_o(C::TILES - 1) + half * (D / 2) + c * 32, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              r[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), f1, __uint_as_float(r[e]) * f0));
           }
           const float* f = reinterpret_cast<const float*>(r);
           const size_t to = at * D + half * (D / 2) + c * 32;
@@ -810,11 +860,11 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
   }
 }
 
-template <int D, class E>
+template <int D, class E, bool SOLO>
 cudaError_t launch_t(const void* q, const CUtensorMap& km, const CUtensorMap& vm,
                      const PrefillParams& p, int grid, cudaStream_t stream) {
   using C = P8Cfg<D, E>;
-  auto kern = prefill_page8_kernel<D, E>;
+  auto kern = prefill_page8_kernel<D, E, SOLO>;
   static std::atomic<uint64_t> configured{0};
   const cudaError_t e = once_per_device(configured, [&] {
     // the warpgroups' register split assumes this launch allocation
@@ -830,26 +880,28 @@ cudaError_t launch_t(const void* q, const CUtensorMap& km, const CUtensorMap& vm
 }
 
 template <class E>
-cudaError_t launch_d(int head_dim, const void* q, const CUtensorMap& km,
+cudaError_t launch_d(int head_dim, bool solo, const void* q, const CUtensorMap& km,
                      const CUtensorMap& vm, const PrefillParams& p, int grid, cudaStream_t stream) {
   switch (head_dim) {
-    case 64: return launch_t<64, E>(q, km, vm, p, grid, stream);
-    case 128: return launch_t<128, E>(q, km, vm, p, grid, stream);
-    case 256: return launch_t<256, E>(q, km, vm, p, grid, stream);
+    case 64: return solo ? launch_t<64, E, true>(q, km, vm, p, grid, stream)
+                         : launch_t<64, E, false>(q, km, vm, p, grid, stream);
+    case 128: return solo ? launch_t<128, E, true>(q, km, vm, p, grid, stream)
+                          : launch_t<128, E, false>(q, km, vm, p, grid, stream);
+    case 256: return launch_t<256, E, false>(q, km, vm, p, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_prefill_page8(int head_dim, int dtype, const void* q,
+cudaError_t launch_prefill_page8(int head_dim, int dtype, bool solo, const void* q,
                                  const CUtensorMap& km, const CUtensorMap& vm,
                                  const PrefillParams& p, int num_sms, cudaStream_t stream) {
   const int grid = p.n_items < num_sms ? p.n_items : num_sms;
   if (grid <= 0) return cudaSuccess;
   switch (dtype) {
-    case FI_DTYPE_BF16: return launch_d<Bf16>(head_dim, q, km, vm, p, grid, stream);
-    case FI_DTYPE_FP16: return launch_d<Fp16>(head_dim, q, km, vm, p, grid, stream);
+    case FI_DTYPE_BF16: return launch_d<Bf16>(head_dim, solo, q, km, vm, p, grid, stream);
+    case FI_DTYPE_FP16: return launch_d<Fp16>(head_dim, solo, q, km, vm, p, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }
