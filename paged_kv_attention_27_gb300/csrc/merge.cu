@@ -31,7 +31,12 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeParams p) {
   for (int idx = threadIdx.x; idx < p.H * q4; idx += kMergeThreads) {
     const int h = idx / q4, c = idx % q4;
     float M = -INFINITY;
-    for (int i = 0; i < n; ++i) M = fmaxf(M, p.s[size_t(base + i) * p.H + h]);
+    bool nan = false;   // (fmaxf passes over a NaN: a NaN state makes the row NaN)
+    for (int i = 0; i < n; ++i) {
+      const float s = p.s[size_t(base + i) * p.H + h];
+      nan |= s != s;
+      M = fmaxf(M, s);
+    }
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sw = 0.f;
     if (M != -INFINITY) {
@@ -47,14 +52,15 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeParams p) {
         sw += w;
       }
     }
-    const float inv = sw > 0.f ? 1.f / sw : 0.f;
+    if (nan) sw = __uint_as_float(0x7fc00000u);
+    const float inv = sw > 0.f ? 1.f / sw : nan ? sw : 0.f;
     uint2 packed;
     packed.x = E::pack2(acc.x * inv, acc.y * inv);
     packed.y = E::pack2(acc.z * inv, acc.w * inv);
     reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) +
                              (size_t(out_row) * p.H + h) * p.d)[c] = packed;
     if (c == 0 && p.lse)
-      p.lse[size_t(out_row) * p.H + h] = sw > 0.f ? M + lg2(sw) * kLn2 : -INFINITY;
+      p.lse[size_t(out_row) * p.H + h] = sw > 0.f ? M + lg2(sw) * kLn2 : nan ? sw : -INFINITY;
   }
 }
 

@@ -427,3 +427,18 @@ def test_decode_nan_rows_of_split_requests_stay_nan():
     assert np.array_equal(torch.isnan(out).all(dim=2).cpu().numpy(), want)
     assert np.array_equal(torch.isnan(out).any(dim=2).cpu().numpy(), want)
     assert np.array_equal(torch.isnan(lse).cpu().numpy(), want)
+
+
+def test_prefill_nan_rows_of_split_items_stay_nan():
+    import torch
+    b = _page8.Batch([5000], 8, 2, 128, 16, qo_lens=[20], seed=35)
+    assert B.fi_plan_get_info(b.plan(B, 152))["num_partial_slots"] > 0
+    b.q[3, 1, 5] = float("nan")
+    b.q[19, 6, 0] = float("inf")
+    d = _page8.Device(b, 152)
+    out, lse = d.run()
+    want = np.zeros((20, 8), dtype=bool)
+    want[3, 1] = want[19, 6] = True
+    assert np.array_equal(torch.isnan(out).all(dim=2).cpu().numpy(), want)
+    assert np.array_equal(torch.isnan(out).any(dim=2).cpu().numpy(), want)
+    assert np.array_equal(torch.isnan(lse).cpu().numpy(), want)
