@@ -56,6 +56,12 @@ struct Fp16 {
   __device__ static __forceinline__ uint16_t one(float x) {
     return __half_as_ushort(__float2half_rn(x));
   }
+  // a - b of packed pairs
+  __device__ static __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a),
+                              *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&d);
+  }
   __device__ static __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4],
                                                   uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -98,6 +104,13 @@ struct E4m3 {
         : "=r"(r.x), "=r"(r.y)
         : "r"(w));
     return r;
+  }
+  // an fp16 pair -> two packed e4m3 in the low 16 bits, as from_f32x2
+  __device__ static __forceinline__ uint32_t from_f16x2(uint32_t h) {
+    __half2_raw r;
+    r.x = uint16_t(h & 0xffffu);
+    r.y = uint16_t(h >> 16);
+    return uint32_t(__nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3));
   }
   // two floats -> two packed e4m3 in the low 16 bits (a in the low byte),
   // rounded to nearest even, finite values saturated at +-448

@@ -90,7 +90,7 @@ struct P8Cfg {
   static constexpr int W_MMA = SOFT, W_KV = SOFT + 2, W_WIDE = SOFT + 4;
   static constexpr int THREADS = 32 * (SOFT + 8);
   // registers per thread at launch and, per warpgroup, after the split
-  static constexpr uint32_t LAUNCH_REGS = 128, SOFT_REGS = 160, HELP_REGS = 96, WIDE_REGS = 96;
+  static constexpr uint32_t LAUNCH_REGS = 128, SOFT_REGS = 160, HELP_REGS = 80, WIDE_REGS = 112;
   static_assert(2 * SOFT_REGS + HELP_REGS + WIDE_REGS <= 4 * LAUNCH_REGS, "");
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t col_s(int i) { return uint32_t(i * N); }
@@ -250,75 +250,129 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
     };
     bool ok = true;
     int gt = 0;   // tiles of earlier items
-    for (int n = 0; ok; ++n) {
-      int it = -1;
-      ok = take_item(n, it);
-      if (!ok || it < 0) break;
-      const WorkItem w = prm.items[it];
+    const int g_log = __ffs(g) - 1;   // g is a power of two
+    int it = -1, it_next = -1;
+    ok = take_item(0, it);
+    WorkItem w, wn;
+    if (ok && it >= 0) w = prm.items[it];
+    for (int n = 0; ok && it >= 0; ++n) {
       const int nt = tiles_of(w);
-      // ---- q as terms: D / 16 lanes per row, 16 elements each
-      if (n >= 1 && !mbar_sleep_warp(smem_u32(&bars.q_empty), (n - 1) & 1, limit, &abort_flag)) {
-        ok = false;
-        break;
-      }
+      // the item's M rows: query rows x heads, heads inner
+      auto m_rows = [&](const WorkItem& y) {
+        return min(C::TILES * C::M, (prm.qo_indptr[y.req + 1] - y.q_row) << g_log);
+      };
+      // The next item, when this one's work is under way: its q into L2.
+      auto look_ahead = [&] {
+        if (!take_item(n + 1, it_next)) return false;
+        if (it_next >= 0) {
+          wn = prm.items[it_next];
+          const int lines = m_rows(wn) * (D * 2 / 128);
+          for (int i = ct; i < lines; i += 128) {
+            const int x = i / (D * 2 / 128);
+            const uint16_t* at = reinterpret_cast<const uint16_t*>(q) +
+                                 (size_t(wn.q_row + (x >> g_log)) * prm.num_qo_heads + wn.head * g +
+                                  (x & (g - 1))) * D + i % (D * 2 / 128) * 64;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+          }
+        }
+        return true;
+      };
+      // ---- q as terms: D / 16 lanes per row, 16 elements each; two rows' loads
+      // ahead of the two rows at work, the first ones before the previous item
+      // has let go of q (loaded row by row and in 32-bit arithmetic this took 29K
+      // cycles, and the item waited for 20K of them)
       {
-        constexpr int LPR = D / 16, RPW = 32 / LPR;
-        const int q_end = prm.qo_indptr[w.req + 1];
-        const int ch = lane % LPR;
-#pragma unroll 2
-        for (int x = ct / LPR; x < C::TILES * C::M; x += 4 * RPW) {
-          const int i = x / C::M, row = x % C::M;
-          const int q_row = w.q_row + i * R + row / g;
-          uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-          if (q_row < q_end) {
-            const uint4* src = reinterpret_cast<const uint4*>(
-                reinterpret_cast<const uint16_t*>(q) +
-                (size_t(q_row) * prm.num_qo_heads + w.head * g + row % g) * D + ch * 16);
-            u[0] = src[0];
-            u[1] = src[1];
-          }
-          float f[16];
-          unpack8<E>(u[0], *reinterpret_cast<float(*)[8]>(f));
-          unpack8<E>(u[1], *reinterpret_cast<float(*)[8]>(f + 8));
-          float a = 0.f;
+        constexpr int LPR = D / 16, STEP_ROWS = 128 / LPR, PASSES = C::TILES * C::M / STEP_ROWS;
+        constexpr int BATCH = 2;
+        static_assert(PASSES % BATCH == 0, "");
+        const int used = m_rows(w);       // (rows behind the last one are never stored)
+        const int ch = lane % LPR, x0 = ct / LPR;
+        uint4 u[BATCH][2];
+        auto load = [&](int b) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float b = fabsf(f[e]);
-            a = b < INFINITY ? fmaxf(a, b) : a;
-          }
-#pragma unroll
-          for (int d = LPR / 2; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-          // the smallest k >= -100 with a <= 448 * 2^k
-          const uint32_t au = __float_as_uint(a);
-          const int k = max(int(au >> 23) - 127 - 8 + ((au & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
-          const float up = __uint_as_float(uint32_t(127 - k) << 23);
-#pragma unroll
-          for (int e = 0; e < 16; ++e)   // (the conversion saturates infinities: NaN instead)
-            f[e] = fabsf(f[e]) < INFINITY ? f[e] * up : __uint_as_float(0x7fc00000u);
-          const int sw = C::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
-          const uint32_t dst = base + C::OFF_Q + i * C::Q + (ch >> 3) * C::M * 128 + row * C::ROWB +
-                               (((ch & 7) ^ sw) << 4);
-#pragma unroll
-          for (int tm = 0; tm < C::TERMS; ++tm) {
-            uint32_t code[4];
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const uint32_t c = E4m3::from_f32x2(f[e], f[e + 1]);
-              const uint32_t h = E4m3::to_f16x2(c);
-              f[e] -= Fp16::lo(h);
-              f[e + 1] -= Fp16::hi(h);
-              if (e % 4 == 0) code[e / 4] = c;
-              else code[e / 4] |= c << 16;
+          for (int e = 0; e < BATCH; ++e) {
+            const int x = x0 + (b * BATCH + e) * STEP_ROWS;
+            u[e][0] = u[e][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (x < used) {
+              const uint4* src = reinterpret_cast<const uint4*>(
+                  reinterpret_cast<const uint16_t*>(q) +
+                  (size_t(w.q_row + (x >> g_log)) * prm.num_qo_heads + w.head * g + (x & (g - 1))) * D +
+                  ch * 16);
+              u[e][0] = src[0];
+              u[e][1] = src[1];
             }
-            st_shared_v4(dst + tm * C::QT, make_uint4(code[0], code[1], code[2], code[3]));
           }
-          if (ch == 0) q_exp[n & 1][x] = uint8_t(k + 128);
+        };
+        load(0);
+        if (n >= 1 && !mbar_sleep_warp(smem_u32(&bars.q_empty), (n - 1) & 1, limit, &abort_flag)) {
+          ok = false;
+          break;
+        }
+#pragma unroll 1
+        for (int b = 0; b * BATCH * STEP_ROWS < used; ++b) {
+          uint4 v[BATCH][2];
+#pragma unroll
+          for (int e = 0; e < BATCH; ++e) {
+            v[e][0] = u[e][0];
+            v[e][1] = u[e][1];
+          }
+          load(b + 1);
+#pragma unroll
+          for (int e4 = 0; e4 < BATCH; ++e4) {
+            const int x = x0 + (b * BATCH + e4) * STEP_ROWS;
+            const int i = x / C::M, row = x % C::M;
+            const uint32_t q2[8] = {v[e4][0].x, v[e4][0].y, v[e4][0].z, v[e4][0].w,
+                                    v[e4][1].x, v[e4][1].y, v[e4][1].z, v[e4][1].w};
+            // |x| of bf16 and fp16 orders as its 15 bits
+            uint32_t top2 = 0u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top2 = __vmaxu2(top2, q2[e] & 0x7fff7fffu);
+#pragma unroll
+            for (int d = LPR / 2; d > 0; d >>= 1)
+              top2 = __vmaxu2(top2, __shfl_xor_sync(0xffffffffu, top2, d));
+            const uint32_t top = max(top2 >> 16, top2 & 0xffffu);
+            constexpr uint32_t kInf = std::is_same<E, Bf16>::value ? 0x7f80u : 0x7c00u;
+            const bool odd = top >= kInf;   // a NaN or an infinity in the row
+            // the smallest k >= -100 with a <= 448 * 2^k (such a row is NaN whatever its k)
+            const uint32_t au = odd ? 0x3f800000u : __float_as_uint(E::lo(top));
+            const int k = max(int(au >> 23) - 127 - 8 + ((au & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+            const float up = __uint_as_float(uint32_t(127 - k) << 23);
+            uint32_t h2[8];                 // the row as fp16 pairs: exact, above its grid of 2^-24
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h2[e] = Fp16::pack2(E::lo(q2[e]) * up, E::hi(q2[e]) * up);
+            if (odd) {   // (the conversion to e4m3 saturates infinities: NaN instead)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if ((q2[e] & 0x7fffu) >= kInf) h2[e] = (h2[e] & 0xffff0000u) | 0x7e00u;
+                if ((q2[e] >> 16 & 0x7fffu) >= kInf) h2[e] = (h2[e] & 0xffffu) | 0x7e000000u;
+              }
+            }
+            const int sw = C::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
+            const uint32_t dst = base + C::OFF_Q + i * C::Q + (ch >> 3) * C::M * 128 +
+                                 row * C::ROWB + (((ch & 7) ^ sw) << 4);
+#pragma unroll
+            for (int tm = 0; tm < C::TERMS; ++tm) {
+              uint32_t code[4];
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                const uint32_t c0 = E4m3::from_f16x2(h2[e]), c1 = E4m3::from_f16x2(h2[e + 1]);
+                code[e / 2] = c0 | (c1 << 16);
+                if (tm + 1 < C::TERMS) {   // what the term leaves, exactly
+                  h2[e] = Fp16::sub2(h2[e], E4m3::to_f16x2(c0));
+                  h2[e + 1] = Fp16::sub2(h2[e + 1], E4m3::to_f16x2(c1));
+                }
+              }
+              st_shared_v4(dst + tm * C::QT, make_uint4(code[0], code[1], code[2], code[3]));
+            }
+            if (ch == 0) q_exp[n & 1][x] = uint8_t(k + 128);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
       }
       float ref = 1.f;
+      if (nt == 0) ok = look_ahead();
       for (int j = 0; j < nt; ++j) {
         const int t = gt + j, ks = t % C::NK, rs = t % C::NVR, st = t & 1;
         const int valid = min(C::N, w.tok_end - w.tok_begin - j * C::N);
@@ -359,8 +413,14 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
           mbar_arrive(smem_u32(&bars.vr_empty[rs]));
           mbar_arrive(smem_u32(&bars.v_full[st]));
         }
+        if (j == 0 && !look_ahead()) {
+          ok = false;
+          break;
+        }
       }
       gt += nt;
+      w = wn;
+      it = it_next;
     }
     if (!ok && lane == 0) fail();
   } else if (warp >= C::W_MMA) {
