@@ -14,6 +14,7 @@
 
 #include "fi_internal.h"
 #include "kernels.cuh"
+#include "page8.cuh"
 
 namespace {
 
@@ -444,6 +445,7 @@ fi_status run_paged(fi_plan_t plan, bool prefill_call, const void* q, const int3
       (k_head_scale && !aligned(k_head_scale, 4)) || (v_head_scale && !aligned(v_head_scale, 4)))
     return FI_ERR_INVALID_ARG;
   const bool page8 = P.kv_dtype == FI_DTYPE_E4M3_PAGE;   // page scales are required
+  const bool solo = static_cast<const fi::PlanHandle*>(plan)->prefill_solo;
   if (page8 && (!k_head_scale || !v_head_scale)) return FI_ERR_INVALID_ARG;
   fi_status st = check_run_scalars(P, kv_layout, page_stride_elems, sm_scale, k_scale, v_scale);
   if (st != FI_OK) return st;
@@ -593,7 +595,7 @@ fi_status run_paged(fi_plan_t plan, bool prefill_call, const void* q, const int3
       dstream = side.stream;
     }
     if (!P.prefill_items.empty()) {
-      e = page8 ? fi::launch_prefill_page8(P.head_dim, P.dtype, P.prefill_solo, q, kmap, vmap, pp,
+      e = page8 ? fi::launch_prefill_page8(P.head_dim, P.dtype, solo, q, kmap, vmap, pp,
                                            P.num_sms, stream)
                 : fi::launch_prefill(P.head_dim, P.dtype, qmap, kmap, vmap, pp, P.num_sms, stream);
       if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
@@ -682,7 +684,7 @@ fi_status fi_plan(int32_t mode, int32_t batch_size, const int32_t* qo_indptr_h,
                   int32_t num_sms, fi_plan_t* out_plan, size_t* workspace_bytes) {
   if (!out_plan || !workspace_bytes) return FI_ERR_INVALID_ARG;
   *out_plan = nullptr;
-  fi_plan_s* p = new (std::nothrow) fi_plan_s;
+  fi::PlanHandle* p = new (std::nothrow) fi::PlanHandle;
   if (!p) return FI_ERR_INVALID_ARG;
   fi_status st = fi::build_plan(mode, batch_size, qo_indptr_h, page_indptr_h, last_page_len_h,
                                 num_qo_heads, num_kv_heads, head_dim, page_size, causal, options,
@@ -692,13 +694,14 @@ fi_status fi_plan(int32_t mode, int32_t batch_size, const int32_t* qo_indptr_h,
     return st;
   }
   const fi::Plan& P = p->p;
+  p->prefill_solo = fi::page8_prefill_solo(P, qo_indptr_h);
   *out_plan = p;
   *workspace_bytes = P.ws.total;
   return FI_OK;
 }
 
 fi_status fi_plan_destroy(fi_plan_t plan) {
-  delete plan;
+  delete static_cast<fi::PlanHandle*>(plan);
   return FI_OK;
 }
 

@@ -20,7 +20,7 @@
 #include <type_traits>
 
 #include "elem.cuh"
-#include "kernels.cuh"
+#include "page8.cuh"
 
 namespace fi {
 

@@ -23,8 +23,9 @@
 //   w = 2^(s + log2 s_v - m),  m the running maximum of s + log2 s_v,
 //   O = sum w code,  l = sum w r / s_v (r: s_v of the item's first page),
 //   out = O r / l,   lse = ln 2 (m + log2 l - log2 r):
-// one exponential per score, and both sums keep their leading bits whatever
-// the spread of the scales.
+// one exponential per score, and both sums keep their leading bits where a
+// request's V scales are up to 2^80 apart (l then stays below 2^118, and a
+// weight of 2^-80 is far from underflow).
 //
 // Roles (8 warps): 0-3 softmax (thread = key of the tile = TMEM lane), then
 // the epilogue (thread = dimension); 4 copies pages by TMA and page scales by
@@ -38,9 +39,8 @@
 #include <type_traits>
 
 #include "elem.cuh"
-#include "fi_internal.h"
-#include "kernels.cuh"
-#include "ptx.cuh"
+#include "page8.cuh"
+#include "ptx_page8.cuh"
 
 namespace fi {
 

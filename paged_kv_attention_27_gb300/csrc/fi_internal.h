@@ -57,22 +57,8 @@ constexpr size_t kAlign = 256;
 // Error bits in the first word of the workspace.
 constexpr uint32_t kErrTimeout = 1u;
 constexpr uint32_t kErrBounds = 2u;
-constexpr uint32_t kErrPages = 4u;
-
-// Step workspace (fi_page_table_step, fi_append_paged_kv): the error word, and
-// the ticket counter of fi_page_table_step's blocks at this offset.
-constexpr size_t kStepTicketOffset = 64;
-constexpr int32_t kStepMaxBatch = 8192;
-constexpr int32_t kStepMaxRequests = 262144;
-constexpr int32_t kStepMaxPageSize = 1024;
-constexpr int32_t kStepMaxEntries = 1 << 30;   // of the ring, page_indices, slot_map
 
 inline int decode_tile_tokens(int head_dim) { return 8192 / head_dim; }  // 32 KB of K+V
-// The kernels over a page-scaled FP8 cache: tokens per tile of the decode
-// kernel; M rows (query rows x the g heads of a kv head) of a prefill item.
-constexpr int kPage8DecodeTile = 128;
-inline int page8_decode_ctas(int head_dim) { return head_dim <= 128 ? 2 : 1; }   // per SM
-inline int page8_prefill_rows(int head_dim) { return head_dim <= 128 ? 256 : 128; }
 // A batch with both decode rows and multi-row (chunked prefill) requests runs
 // as one persistent launch of the mixed kernel for these shapes (q/out and
 // cache of one 16-bit type, head_dim 256, 1, 2 or 4 query heads per kv head).
@@ -126,8 +112,6 @@ struct Plan {
   std::vector<WorkItem> prefix_items;
   std::vector<int32_t> prefix_tables;
   int32_t num_prefix_groups = 0;
-  // page-scaled prefill: much of the work is in items of one M tile
-  bool prefill_solo = false;
   int32_t chunk_tokens = 0;
   int32_t num_split = 0;
   int32_t num_slots = 0;

@@ -131,75 +131,6 @@ cudaError_t launch_mixed(int head_dim, int group, int dtype, const CUtensorMap& 
 cudaError_t launch_decode(int head_dim, int group, int dtype, int kv_dtype, const CUtensorMap& km,
                           const CUtensorMap& vm, const DecodeParams& p, int n_items, int num_sms,
                           cudaStream_t stream);
-// Over a page-scaled FP8 cache (decode_page8.cu, prefill_page8.cu); the
-// params' k_head_scale / v_head_scale are then [num_pages][num_kv_heads].
-cudaError_t launch_decode_page8(int head_dim, int group, int dtype, const CUtensorMap& km,
-                                const CUtensorMap& vm, const DecodeParams& p, int n_items,
-                                int num_sms, cudaStream_t stream);
-// solo: items whose rows fill one of the two M tiles share it between both
-// streams (Plan::prefill_solo)
-cudaError_t launch_prefill_page8(int head_dim, int dtype, bool solo, const void* q,
-                                 const CUtensorMap& km, const CUtensorMap& vm,
-                                 const PrefillParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_merge(const MergeParams& p, int n_rows, cudaStream_t stream);
-
-// A small work-list image as a kernel parameter (merge.cu): one launch in
-// place of a staging copy. `bytes` is a multiple of 16, at most the capacity.
-constexpr size_t kImageParamBytes = 3840;
-struct ImageParam {
-  uint32_t words[kImageParamBytes / 4];
-};
-cudaError_t launch_image(const ImageParam& image, size_t bytes, void* dst, cudaStream_t stream);
-
-// fi_page_table_step (page_step.cu): the arguments of the call, and the step
-// workspace's error word and ticket.
-struct PageStepParams {
-  int32_t batch;
-  const int32_t* slots;
-  const int32_t* new_len;
-  int32_t max_requests;
-  int32_t max_pages;
-  int32_t page_size;
-  const int32_t* kv_len;
-  int32_t* kv_len_out;
-  int32_t* block_table;
-  int32_t* free_ring;
-  int32_t ring_capacity;
-  const int32_t* ring_state;
-  int32_t* ring_state_out;
-  int32_t* page_indptr;
-  int32_t* page_indices;
-  int32_t page_capacity;
-  int32_t* last_page_len;
-  int32_t* qo_indptr;
-  int64_t* slot_map;
-  int32_t* positions;
-  int32_t token_capacity;
-  uint32_t* err;
-  uint32_t* ticket;
-};
-cudaError_t launch_page_step(const PageStepParams& p, cudaStream_t stream);
-
-// fi_append_paged_kv (append.cu). Strides in elements: of a token row of k/v,
-// and of the cache's pages, slots and kv heads.
-struct AppendParams {
-  int32_t num_tokens;
-  const int64_t* slot_map;
-  const void* k_new;
-  const void* v_new;
-  int64_t token_stride;
-  int32_t num_kv_heads;
-  void* k_cache;
-  void* v_cache;
-  int64_t page_stride, slot_stride, head_stride;
-  int32_t num_pages;
-  int32_t page_size;
-  float* k_scale;
-  float* v_scale;
-  uint32_t* err;
-};
-// kv_dtype: dtype (the rows are copied) or FI_DTYPE_E4M3_PAGE
-cudaError_t launch_append(int head_dim, int dtype, int kv_dtype, const AppendParams& p,
-                          cudaStream_t stream);
 
 }  // namespace fi

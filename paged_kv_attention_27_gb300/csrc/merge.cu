@@ -5,6 +5,7 @@
 // Used both as the ABI call fi_merge_states and after split-KV decode.
 #include "elem.cuh"
 #include "kernels.cuh"
+#include "page8.cuh"
 #include "ptx.cuh"
 
 namespace fi {

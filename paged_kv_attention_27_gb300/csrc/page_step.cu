@@ -17,7 +17,7 @@
 // by the last block of a ticket counter (which wraps to zero) otherwise.
 #include <cuda_runtime.h>
 
-#include "kernels.cuh"
+#include "page8.cuh"
 
 namespace fi {
 

@@ -12,6 +12,7 @@
 #include <cstring>
 
 #include "fi_internal.h"
+#include "page8.h"
 
 namespace fi {
 
@@ -330,17 +331,6 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
     return x.b != y.b ? x.b < y.b : x.qt < y.qt;
   });
 
-  if (page8 && head_dim <= 128) {
-    // work (keys) in items whose rows fill one M tile (128 / g rows)
-    int64_t one = 0, all = 0;
-    for (const Tile& t : tiles) {
-      const int64_t rows = std::min<int64_t>(tile_rows, qo_len[t.b] - int64_t(t.qt) * tile_rows);
-      all += t.len;
-      if (rows * g <= kPrefillTileM) one += t.len;
-    }
-    p.prefill_solo = one * 8 > all;
-  }
-
   // ---- KV split of prefill tiles when the launch has under two waves of
   //      work units (a CTA's unit: a tile with one head, or with a head pair
   //      on the two-tile kernel). Long tiles are then cut into pieces of
@@ -467,6 +457,21 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
 
   *out = std::move(p);
   return FI_OK;
+}
+
+bool page8_prefill_solo(const Plan& p, const int32_t* qo_indptr) {
+  if (p.kv_dtype != FI_DTYPE_E4M3_PAGE || p.head_dim > 128 || p.prefill_items.empty()) return false;
+  // work (keys) in items whose rows fill one M tile, of all; the items of a
+  // tile's kv heads follow one another
+  const int32_t rows_of_one = kPrefillTileM / (p.num_qo_heads / p.num_kv_heads);
+  int64_t one = 0, all = 0;
+  for (size_t i = 0; i < p.prefill_items.size(); i += size_t(p.num_kv_heads)) {
+    const WorkItem& w = p.prefill_items[i];
+    const int64_t len = w.tok_end - w.tok_begin;
+    all += len;
+    if (qo_indptr[w.req + 1] - w.q_row <= rows_of_one) one += len;
+  }
+  return one * 8 > all;
 }
 
 }  // namespace fi

@@ -26,8 +26,9 @@
 //   w = 2^(s + log2 s_v - m),  m the running maximum of s + log2 s_v,
 //   O = sum w code,  l = sum w r / s_v (r: s_v of the item's first page),
 //   out = O r / l,   lse = ln 2 (m + log2 l - log2 r):
-// one exponential per score, and both sums keep their leading bits whatever
-// the spread of the scales.
+// one exponential per score, and both sums keep their leading bits where a
+// request's V scales are up to 2^80 apart (l then stays below 2^118, and a
+// weight of 2^-80 is far from underflow).
 //
 // Roles (16 warps): 8 softmax warps, then the epilogue. They work on one M tile
 // after the other, two threads per row (TMEM lane), each on half of the keys:
@@ -41,9 +42,8 @@
 #include <type_traits>
 
 #include "elem.cuh"
-#include "fi_internal.h"
-#include "kernels.cuh"
-#include "ptx.cuh"
+#include "page8.cuh"
+#include "ptx_page8.cuh"
 
 namespace fi {
 
@@ -57,8 +57,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // at or below 2^8, inside fp16
 constexpr float kRescaleThreshold = 8.0f;
 constexpr int kItemRing = 8;
-// tiles whose page scales are kept: K of tile t is widened once S of tile t - 2
-// is complete, which was issued after the softmax of tile t - 3
+// tiles whose page scales are kept: K of tile t is copied once S of tile t - 3
+// is complete, which was issued after the softmax of tile t - 4
 constexpr int kScaleRing = 4;
 
 template <int D, class E>
