@@ -269,6 +269,12 @@ fi_status fi_plan_get_work(fi_plan_t plan, int32_t* items_h, int32_t capacity,
  *                    stored ones). NULL means 1 for every head. The values
  *                    must be finite and > 0 (caller contract: they are read
  *                    on the device only); 4-byte aligned.
+ *                    An FI_DTYPE_E4M3_PAGE plan needs both (NULL is
+ *                    FI_ERR_INVALID_ARG), as [num_pages][num_kv_heads]: the
+ *                    factor of each page and kv head. They must be in 2^-120
+ *                    .. 2^120, and those of V of one request and kv head at
+ *                    most a factor of 2^80 apart; those of pages that no
+ *                    request holds are not read.
  *   out              device [B][num_qo_heads][head_dim], the plan's dtype.
  *   lse              device fp32 [B][num_qo_heads] or NULL.
  *   workspace        device buffer of at least the planned size, 256-byte

@@ -442,3 +442,70 @@ def test_prefill_nan_rows_of_split_items_stay_nan():
     assert np.array_equal(torch.isnan(out).all(dim=2).cpu().numpy(), want)
     assert np.array_equal(torch.isnan(out).any(dim=2).cpu().numpy(), want)
     assert np.array_equal(torch.isnan(lse).cpu().numpy(), want)
+
+
+# ---- both ----------------------------------------------------------------------------------------
+@pytest.mark.parametrize("prefill", [False, True])
+@pytest.mark.parametrize("g,d,P", [(8, 128, 16), (1, 64, 32), (4, 256, 16)])
+def test_value_scales_2_80_apart(g, d, P, prefill):
+    """Neighbouring pages' V scales differ by the documented 2^80, the first
+    page's being the smaller or the larger one."""
+    b = _page8.Batch([500, 70, 16], 2 * g, 2, d, P, qo_lens=[30, 70, 5] if prefill else None, seed=16)
+    up = np.arange(len(b.page_indices)) % 2 == 0
+    b.scale[1][b.page_indices[up]] *= 2.0 ** 40
+    b.scale[1][b.page_indices[~up]] *= 2.0 ** -40
+    _check(b, what="2^80 apart")
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+def test_two_streams_at_once_with_one_plan(prefill):
+    import torch
+    qo = [200, 1, 17, 300] if prefill else None
+    b = _page8.Batch([3000, 64, 333, 1800], 16, 2, 128, 16, qo_lens=qo, seed=17)
+    x, y = _page8.Device(b), _page8.Device(b)
+    y.plan = x.plan
+    want = x.run()[0].clone()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for d, s in zip((x, y), streams):
+            with torch.cuda.stream(s):
+                d.out.fill_(7)
+                d.run()
+    torch.cuda.synchronize()
+    for d in (x, y):
+        assert d.status() == B.FI_OK and torch.equal(d.out, want)
+
+
+def test_cache_offsets_beyond_32_bits():
+    """Pages 2^28 bytes apart: append to and attention over a cache whose offsets
+    pass 2^32."""
+    import torch
+    P, H, d = 16, 2, 128
+    stride = 1 << 28
+    buf = torch.empty(18 * stride, dtype=torch.uint8, device="cuda")
+    for qo in (None, [40, 9]):
+        b = _page8.Batch([170, 60], 8, H, d, P, qo_lens=qo, seed=18, spare=2)
+        assert b.num_pages * stride > 1 << 32
+        x = _page8.Device(b)
+        k = buf.as_strided((b.num_pages, P, H, d), (stride, H * d, d, 1))
+        v = k.as_strided(k.shape, k.stride(), storage_offset=1 << 20)
+        # the last keys of request 0 come by an append
+        page = int(b.page_indices[b.page_indptr[1] - 1])
+        n = int(b.last_page_len[0])
+        k.copy_(x.k)
+        v.copy_(x.v)
+        k[page], v[page] = 0, 0
+        ws = torch.zeros(B.FI_STEP_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+        kn, vn = [(torch.from_numpy(b.kv64(i)[page, :n]).to(torch.bfloat16)).cuda() for i in (0, 1)]
+        smap = torch.arange(page * P, page * P + n, device="cuda")
+        B.fi_append_paged_kv(n, smap, kn, vn, 0, B.FI_DTYPE_BF16, H, d, k, v, B.FI_DTYPE_E4M3_PAGE,
+                             B.FI_LAYOUT_NHD, stride, b.num_pages, P, x.ks, x.vs, ws)
+        assert B.fi_check_device_status(ws) == B.FI_OK
+        b.scale[0][page], b.scale[1][page] = x.ks[page].cpu().numpy(), x.vs[page].cpu().numpy()
+        b.codes[0][page], b.codes[1][page] = k[page].cpu().numpy(), v[page].cpu().numpy()
+        assert b.codes[0][page, :n].any() and not b.codes[0][page, n:].any()
+        x.k, x.v = k, v
+        out, lse = x.run(page_stride=stride)
+        assert x.status() == B.FI_OK
+        _page8.compare(b, out, lse, _page8.reference(b), what="far pages")

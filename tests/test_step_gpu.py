@@ -166,6 +166,18 @@ def test_largest_batch_and_slots():
     _check(s.step(order, add, 20000, 8192 * 32), want, order, 20000, True)
 
 
+@pytest.mark.parametrize("capacity", [8192, 16384])
+def test_largest_batch_with_few_new_rows(capacity):
+    """(few output entries: the blocks are one cluster)"""
+    s = Server(262144, 2, 16, 20000, 4)
+    rng = np.random.default_rng(10)
+    order = rng.permutation(262144)[:8192]
+    s.fill([0])
+    add = rng.integers(0, 2, 8192)
+    want = s.want(order, add, capacity, capacity)
+    _check(s.step(order, add, capacity, capacity), want, order, capacity, True)
+
+
 @pytest.mark.parametrize("what,status", [
     ("pages", B.FI_ERR_OUT_OF_PAGES), ("row", B.FI_ERR_OUT_OF_PAGES),
     ("page_capacity", B.FI_ERR_OUT_OF_PAGES), ("token_capacity", B.FI_ERR_OUT_OF_PAGES),
