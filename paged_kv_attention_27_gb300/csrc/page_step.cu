@@ -15,6 +15,12 @@
 // ring state may be updated in place: then they are written once all blocks
 // have read them, after a cluster barrier where one cluster has all blocks,
 // by the last block of a ticket counter (which wraps to zero) otherwise.
+//
+// Measured, calls back to back: 256 requests of up to 8K tokens and one new
+// token each (180 KB) 8.2 us, 1536 of 2048 requests with up to 64 new tokens
+// (1.3 MB) 12.3 us. Blocks of 512 threads with 2048 entries each; 1024 threads
+// and 4096 entries took 10.2 and 14.3 us (a barrier waits for twice the warps),
+// 256 threads 8.2 and 14.4 us.
 #include <cuda_runtime.h>
 
 #include "page8.cuh"
@@ -23,8 +29,8 @@ namespace fi {
 
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kPerBlock = 4096;   // output entries per block that the grid is sized for
+constexpr int kThreads = 512;
+constexpr int kPerBlock = 2048;   // output entries per block that the grid is sized for
 constexpr int kMaxBlocks = 152;
 constexpr int kCluster = 8;       // blocks of the largest portable cluster
 constexpr long long kMaxLen = 0x3fffffff;   // INT32_MAX / 2 tokens, as fi_plan accepts
@@ -138,7 +144,9 @@ __global__ void __launch_bounds__(kThreads) page_step_kernel(PageStepParams p) {
   if (err) atomicOr(&err_sh, err);
   __syncthreads();
   // the warps' sums: lane w has those of warps 0..w
-  const Sums warps = warp_scan(warp_sums[lane], lane);
+  constexpr int kWarps = kThreads / 32;
+  const Sums warps =
+      warp_scan(kWarps == 32 || lane < kWarps ? warp_sums[lane % kWarps] : Sums{0u, 0u, 0u, 0u}, lane);
   auto of_lane = [&](int w) {
     return Sums{__shfl_sync(0xffffffffu, warps.take, w), __shfl_sync(0xffffffffu, warps.give, w),
                 __shfl_sync(0xffffffffu, warps.has, w), __shfl_sync(0xffffffffu, warps.rows, w)};
