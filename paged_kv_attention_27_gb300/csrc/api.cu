@@ -116,12 +116,37 @@ void fill_image(uint8_t* dst, const fi::Plan& P) {
   }
 }
 
+// Marks a slot as in use by the work launched on `stream` so far, when it goes
+// out of scope: a run call has its kernels follow the copying kernel without
+// an event between them.
+class SlotInUse {
+ public:
+  SlotInUse() = default;
+  SlotInUse(const SlotInUse&) = delete;
+  SlotInUse& operator=(const SlotInUse&) = delete;
+  void set(Staging* s, int slot, cudaStream_t stream) {
+    s_ = s;
+    slot_ = slot;
+    stream_ = stream;
+  }
+  ~SlotInUse() {
+    if (!s_) return;
+    if (cudaEventRecord(s_->done[slot_], stream_) == cudaSuccess) s_->pending[slot_] = true;
+    else cudaStreamSynchronize(stream_);
+  }
+
+ private:
+  Staging* s_ = nullptr;
+  int slot_ = 0;
+  cudaStream_t stream_ = nullptr;
+};
+
 // Fills `bytes` bytes of a pinned slot of `s` with `fill` and copies them
 // to device `dst` on `stream` (synchronous pageable copy if pinned memory
 // cannot be had).
 template <class Fill>
 fi_status stage_and_copy(Staging& s, void* dst, size_t bytes, Fill fill, cudaStream_t stream,
-                         const char* what) {
+                         const char* what, SlotInUse* later = nullptr) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return FI_ERR_NO_DEVICE;
   if (s.device != dev || bytes > s.slot_bytes) {
@@ -164,6 +189,12 @@ fi_status stage_and_copy(Staging& s, void* dst, size_t bytes, Fill fill, cudaStr
   if (e != cudaSuccess) return cuda_fail(e, what);
   uint8_t* src = s.buf + size_t(i) * s.slot_bytes;
   fill(src);
+  if (later) {
+    e = fi::launch_image_copy(src, bytes, dst, stream);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    later->set(&s, i, stream);
+    return FI_OK;
+  }
   e = cudaMemcpyAsync(dst, src, bytes, cudaMemcpyHostToDevice, stream);
   if (e == cudaSuccess) e = cudaEventRecord(s.done[i], stream);
   if (e != cudaSuccess) return cuda_fail(e, what);
@@ -223,10 +254,13 @@ fi_status host_steps_ready(HostSteps& h) {
 // or not at all (the host-buffer call uploads it with the page table).
 enum class Upload { kStaged, kStatic, kDone };
 
-// A small image of a page-scaled plan goes as a kernel parameter: 4 us less of
-// host time than the staging copy with its events, and the launch behind it
-// waits for a kernel of 1 us instead of the copy engine.
-fi_status upload_image(void* dst, const fi::Plan& P, cudaStream_t stream) {
+// The image of a page-scaled plan goes up by a kernel, beside whose end the
+// attention kernel sets up: 4 to 6 us less a call than the copy engine between
+// two launches (64 requests of 32 heads 136 -> 132 us). A small one is the
+// kernel's parameter (4 us less of host time than a pinned slot with its event;
+// parameters of 32,000 bytes were 7 us slower), a larger one is read from the
+// pinned slot.
+fi_status upload_image(void* dst, const fi::Plan& P, cudaStream_t stream, SlotInUse* later) {
   if (P.kv_dtype == FI_DTYPE_E4M3_PAGE && P.ws.image_end <= fi::kImageParamBytes) {
     fi::ImageParam image;
     fill_image(reinterpret_cast<uint8_t*>(image.words), P);
@@ -234,7 +268,8 @@ fi_status upload_image(void* dst, const fi::Plan& P, cudaStream_t stream) {
     return e == cudaSuccess ? FI_OK : cuda_fail(e, "work-list launch");
   }
   return stage_and_copy(g_staging, dst, P.ws.image_end,
-                        [&](uint8_t* p) { fill_image(p, P); }, stream, "work-list upload");
+                        [&](uint8_t* p) { fill_image(p, P); }, stream, "work-list upload",
+                        P.kv_dtype == FI_DTYPE_E4M3_PAGE ? later : nullptr);
 }
 
 // The work-list upload of the no-allocation decode call: the image is built
@@ -467,7 +502,8 @@ fi_status run_paged(fi_plan_t plan, bool prefill_call, const void* q, const int3
   }
   // Upload header (zeroed error word and counters) + work lists + merge
   // tasks in one copy.
-  if (upload == Upload::kStaged) st = upload_image(ws, P, stream);
+  SlotInUse slot;   // (of the staging ring)
+  if (upload == Upload::kStaged) st = upload_image(ws, P, stream, &slot);
   else if (upload == Upload::kStatic) st = upload_image_static(ws, P, stream);
   if (st != FI_OK) return st;
   cudaError_t e = cudaSuccess;
@@ -596,7 +632,7 @@ fi_status run_paged(fi_plan_t plan, bool prefill_call, const void* q, const int3
     }
     if (!P.prefill_items.empty()) {
       e = page8 ? fi::launch_prefill_page8(P.head_dim, P.dtype, solo, q, kmap, vmap, pp,
-                                           P.num_sms, stream)
+                                           P.num_sms, !both, stream)
                 : fi::launch_prefill(P.head_dim, P.dtype, qmap, kmap, vmap, pp, P.num_sms, stream);
       if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
     }
@@ -613,7 +649,7 @@ fi_status run_paged(fi_plan_t plan, bool prefill_call, const void* q, const int3
       mp.out = out;
       mp.lse = lse;
       mp.dtype = P.dtype;
-      e = fi::launch_merge(mp, int(P.prefill_merges.size()), stream);
+      e = fi::launch_merge_page8(mp, int(P.prefill_merges.size()), page8, stream);
       if (e != cudaSuccess) return cuda_fail(e, "prefill merge launch");
     }
     if (!P.prefix_items.empty()) {
@@ -642,7 +678,7 @@ fi_status run_paged(fi_plan_t plan, bool prefill_call, const void* q, const int3
     }
     if (!P.decode_items.empty()) {
       e = page8 ? fi::launch_decode_page8(P.head_dim, group, P.dtype, kmap, vmap, dp,
-                                          int(P.decode_items.size()), P.num_sms, dstream)
+                                          int(P.decode_items.size()), P.num_sms, !both, dstream)
                 : fi::launch_decode(P.head_dim, group, P.dtype, P.kv_dtype, kmap, vmap, dp,
                                     int(P.decode_items.size()), P.num_sms, dstream);
       if (e != cudaSuccess) return cuda_fail(e, "decode launch");

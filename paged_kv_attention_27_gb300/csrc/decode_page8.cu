@@ -35,6 +35,12 @@
 // item's q into terms. The launch is persistent: a CTA takes items from a
 // counter and the ring runs on from item to item. (With q and the merge on the
 // softmax warps, an item's start and end cost as much as four tiles.)
+//
+// Measured, calls back to back with their work-list copies: 64 requests of
+// 512-4096 keys, 32/32 heads of 128 (828 MB) 132 us, 0.92 of the copy bandwidth;
+// 128 requests of 128-16384 keys, 64/8 heads (870 MB) 152 us, 0.84; 56 requests,
+// 16/8 heads of 256, fp16, window of 4096 (598 MB) 104.6 us, 0.84. Long keys
+// alone run at 0.97-0.99; the rest is items' starts and ends and the last items.
 #include <cfloat>
 #include <type_traits>
 
@@ -151,7 +157,10 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
     return n > 0 ? (n + lead_of(w) + C::T - 1) / C::T : 0;
   };
 
+  // The next kernel of the stream may start its set-up beside this one, as this
+  // one's runs beside the copy of its work list.
   if (threadIdx.x == 0) {
+    pdl_trigger();
     for (int s = 0; s < kItemRing; ++s) {
       mbar_init(smem_u32(&bars.item_full[s]), 1);
       mbar_init(smem_u32(&bars.item_empty[s]), 6);      // 4 softmax warps, the MMA and q warps
@@ -174,12 +183,6 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
     abort_flag = 0;
     fence_barrier_init();
   }
-  // The first item and its pages' ids: on their way during the set-up below.
-  WorkItem w0;
-  w0.req = -1;
-  int page0 = -1;
-  if (warp == 4 || warp == 7) w0 = prm.items[blockIdx.x];   // (the grid has no more CTAs than items)
-  if (warp == 4 && lane < min(ppt, w0.n_pages)) page0 = prm.page_indices[w0.page_begin + lane];
   // rows of Q that no head uses stay zero
   for (int i = threadIdx.x; i < 2 * C::QBYTES / 16; i += C::THREADS)
     st_shared_zero16(base + C::OFF_Q + i * 16);
@@ -188,6 +191,7 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
     tmem_alloc(smem_u32(&tmem_base_sh), C::TMEM_COLS);
     tmem_relinquish();
   }
+  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -197,6 +201,7 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
 
   if (warp == 4) {
     // ---------------------------------------------------------------- producer
+    WorkItem w = prm.items[blockIdx.x], wn;   // (the grid has no more CTAs than items)
     if (lane == 0) {
       prefetch_tensormap(&k_map);
       prefetch_tensormap(&v_map);
@@ -224,9 +229,8 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
     };
     auto pages_in = [&](const WorkItem& w, int j) { return min(ppt, w.n_pages - j * ppt); };
     int g = 0;
-    WorkItem w = w0, wn;
     bool ok = publish(0, w);
-    int next_page = page0;
+    int next_page = lane < pages_in(w, 0) ? prm.page_indices[w.page_begin + lane] : -1;
     for (int n = 0; ok && w.req >= 0; ++n) {
       const int nt = tiles_of(w);
       const int c1 = prm.layout == FI_LAYOUT_NHD ? w.head : 0;
@@ -385,8 +389,9 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
     const int h = lane / LPH, off = lane % LPH * EPL;
     bool ok = true;
     for (int n = 0;; ++n) {
-      WorkItem w = w0;   // (item 0 is read before it is published)
+      WorkItem w;
       if (n > 0) ok = take_item_warp(n, w);
+      else w = prm.items[blockIdx.x];   // (read before it is published)
       if (!ok || w.req < 0) break;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
           reinterpret_cast<const uint16_t*>(prm.q) +
@@ -807,7 +812,7 @@ decode_page8_kernel(const __grid_constant__ CUtensorMap k_map,
 
 template <int D, int G, class E>
 cudaError_t launch_t(const CUtensorMap& km, const CUtensorMap& vm, const DecodeParams& p,
-                     int n_items, int num_sms, cudaStream_t stream) {
+                     int n_items, int num_sms, bool overlap, cudaStream_t stream) {
   using C = D8Cfg<D, G, E>;
   auto kern = decode_page8_kernel<D, G, E>;
   static std::atomic<uint64_t> configured{0};
@@ -818,29 +823,31 @@ cudaError_t launch_t(const CUtensorMap& km, const CUtensorMap& vm, const DecodeP
   DecodeParams q = p;
   q.n_items = n_items;
   const long long slots = (long long)num_sms * C::CTAS;
-  kern<<<int(slots < n_items ? slots : n_items), C::THREADS, C::SMEM, stream>>>(km, vm, q);
-  return cudaGetLastError();
+  return launch_overlapping(kern, int(slots < n_items ? slots : n_items), C::THREADS, C::SMEM,
+                            overlap, stream, km, vm, q);
 }
 
 template <int D, class E>
 cudaError_t launch_g(int group, const CUtensorMap& km, const CUtensorMap& vm,
-                     const DecodeParams& p, int n_items, int num_sms, cudaStream_t stream) {
+                     const DecodeParams& p, int n_items, int num_sms, bool overlap,
+                     cudaStream_t stream) {
   switch (group) {
-    case 1: return launch_t<D, 1, E>(km, vm, p, n_items, num_sms, stream);
-    case 2: return launch_t<D, 2, E>(km, vm, p, n_items, num_sms, stream);
-    case 4: return launch_t<D, 4, E>(km, vm, p, n_items, num_sms, stream);
-    case 8: return launch_t<D, 8, E>(km, vm, p, n_items, num_sms, stream);
+    case 1: return launch_t<D, 1, E>(km, vm, p, n_items, num_sms, overlap, stream);
+    case 2: return launch_t<D, 2, E>(km, vm, p, n_items, num_sms, overlap, stream);
+    case 4: return launch_t<D, 4, E>(km, vm, p, n_items, num_sms, overlap, stream);
+    case 8: return launch_t<D, 8, E>(km, vm, p, n_items, num_sms, overlap, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 template <class E>
 cudaError_t launch_d(int head_dim, int group, const CUtensorMap& km, const CUtensorMap& vm,
-                     const DecodeParams& p, int n_items, int num_sms, cudaStream_t stream) {
+                     const DecodeParams& p, int n_items, int num_sms, bool overlap,
+                     cudaStream_t stream) {
   switch (head_dim) {
-    case 64: return launch_g<64, E>(group, km, vm, p, n_items, num_sms, stream);
-    case 128: return launch_g<128, E>(group, km, vm, p, n_items, num_sms, stream);
-    case 256: return launch_g<256, E>(group, km, vm, p, n_items, num_sms, stream);
+    case 64: return launch_g<64, E>(group, km, vm, p, n_items, num_sms, overlap, stream);
+    case 128: return launch_g<128, E>(group, km, vm, p, n_items, num_sms, overlap, stream);
+    case 256: return launch_g<256, E>(group, km, vm, p, n_items, num_sms, overlap, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -849,11 +856,11 @@ cudaError_t launch_d(int head_dim, int group, const CUtensorMap& km, const CUten
 
 cudaError_t launch_decode_page8(int head_dim, int group, int dtype, const CUtensorMap& km,
                                 const CUtensorMap& vm, const DecodeParams& p, int n_items,
-                                int num_sms, cudaStream_t stream) {
+                                int num_sms, bool overlap, cudaStream_t stream) {
   if (n_items <= 0 || num_sms <= 0) return cudaSuccess;
   switch (dtype) {
-    case FI_DTYPE_BF16: return launch_d<Bf16>(head_dim, group, km, vm, p, n_items, num_sms, stream);
-    case FI_DTYPE_FP16: return launch_d<Fp16>(head_dim, group, km, vm, p, n_items, num_sms, stream);
+    case FI_DTYPE_BF16: return launch_d<Bf16>(head_dim, group, km, vm, p, n_items, num_sms, overlap, stream);
+    case FI_DTYPE_FP16: return launch_d<Fp16>(head_dim, group, km, vm, p, n_items, num_sms, overlap, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -6,7 +6,7 @@
 #include "elem.cuh"
 #include "kernels.cuh"
 #include "page8.cuh"
-#include "ptx.cuh"
+#include "ptx_page8.cuh"
 
 namespace fi {
 
@@ -20,6 +20,8 @@ constexpr int kMergeThreads = 128;
 
 template <class E>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeParams p) {
+  pdl_trigger();
+  pdl_wait();
   const int r = blockIdx.x;
   int out_row = r, base = r * p.S, n = p.S;
   if (p.tasks) {
@@ -69,9 +71,24 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(MergeParams p) {
 __global__ void __launch_bounds__(kImageParamBytes / 16)
 image_kernel(const __grid_constant__ ImageParam image, uint4* dst, int pieces) {
   const int i = threadIdx.x;
+  pdl_trigger();
+  uint4 x = make_uint4(0u, 0u, 0u, 0u);
   if (i < pieces)
-    dst[i] = make_uint4(image.words[4 * i], image.words[4 * i + 1], image.words[4 * i + 2],
-                        image.words[4 * i + 3]);
+    x = make_uint4(image.words[4 * i], image.words[4 * i + 1], image.words[4 * i + 2],
+                   image.words[4 * i + 3]);
+  pdl_wait();   // (an earlier run may still use the workspace)
+  if (i < pieces) dst[i] = x;
+}
+
+constexpr int kCopyThreads = 256;
+__global__ void __launch_bounds__(kCopyThreads)
+image_copy_kernel(const uint4* src, uint4* dst, int64_t pieces) {
+  const int64_t i = int64_t(blockIdx.x) * kCopyThreads + threadIdx.x;
+  pdl_trigger();
+  uint4 x = make_uint4(0u, 0u, 0u, 0u);
+  if (i < pieces) x = __ldcv(src + i);   // (the host writes it anew for each call)
+  pdl_wait();
+  if (i < pieces) dst[i] = x;
 }
 
 }  // namespace
@@ -79,18 +96,31 @@ image_kernel(const __grid_constant__ ImageParam image, uint4* dst, int pieces) {
 cudaError_t launch_image(const ImageParam& image, size_t bytes, void* dst, cudaStream_t stream) {
   const int pieces = int(bytes / 16);
   if (pieces <= 0) return cudaSuccess;
-  image_kernel<<<1, (pieces + 31) / 32 * 32, 0, stream>>>(image, static_cast<uint4*>(dst), pieces);
-  return cudaGetLastError();
+  return launch_overlapping(image_kernel, 1, (pieces + 31) / 32 * 32, 0, true, stream, image,
+                            static_cast<uint4*>(dst), pieces);
+}
+
+cudaError_t launch_image_copy(const void* src, size_t bytes, void* dst, cudaStream_t stream) {
+  const int64_t pieces = int64_t(bytes / 16);
+  if (pieces <= 0) return cudaSuccess;
+  return launch_overlapping(image_copy_kernel, int((pieces + kCopyThreads - 1) / kCopyThreads),
+                            kCopyThreads, 0, true, stream, static_cast<const uint4*>(src),
+                            static_cast<uint4*>(dst), pieces);
+}
+
+cudaError_t launch_merge_page8(const MergeParams& p, int n_rows, bool overlap, cudaStream_t stream) {
+  if (n_rows <= 0 || p.H <= 0) return cudaSuccess;
+  switch (p.dtype) {
+    case FI_DTYPE_BF16:
+      return launch_overlapping(merge_kernel<Bf16>, n_rows, kMergeThreads, 0, overlap, stream, p);
+    case FI_DTYPE_FP16:
+      return launch_overlapping(merge_kernel<Fp16>, n_rows, kMergeThreads, 0, overlap, stream, p);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 cudaError_t launch_merge(const MergeParams& p, int n_rows, cudaStream_t stream) {
-  if (n_rows <= 0 || p.H <= 0) return cudaSuccess;
-  switch (p.dtype) {
-    case FI_DTYPE_BF16: merge_kernel<Bf16><<<n_rows, kMergeThreads, 0, stream>>>(p); break;
-    case FI_DTYPE_FP16: merge_kernel<Fp16><<<n_rows, kMergeThreads, 0, stream>>>(p); break;
-    default: return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
+  return launch_merge_page8(p, n_rows, false, stream);
 }
 
 }  // namespace fi

@@ -1,6 +1,8 @@
 // Launches of the kernels over a page-scaled FP8 cache and of the calls that
 // prepare a step.
 #pragma once
+#include <type_traits>
+
 #include "kernels.cuh"
 #include "page8.h"
 
@@ -8,22 +10,47 @@ namespace fi {
 
 // Over a page-scaled FP8 cache (decode_page8.cu, prefill_page8.cu); the
 // params' k_head_scale / v_head_scale are then [num_pages][num_kv_heads].
+// overlap: the launch may start beside the one in front of it (the copy of its
+// work list), for which the kernels wait after their set-up.
 cudaError_t launch_decode_page8(int head_dim, int group, int dtype, const CUtensorMap& km,
                                 const CUtensorMap& vm, const DecodeParams& p, int n_items,
-                                int num_sms, cudaStream_t stream);
+                                int num_sms, bool overlap, cudaStream_t stream);
 // solo: items whose rows fill one of the two M tiles share it between both
 // streams (PlanHandle::prefill_solo)
 cudaError_t launch_prefill_page8(int head_dim, int dtype, bool solo, const void* q,
                                  const CUtensorMap& km, const CUtensorMap& vm,
-                                 const PrefillParams& p, int num_sms, cudaStream_t stream);
+                                 const PrefillParams& p, int num_sms, bool overlap,
+                                 cudaStream_t stream);
 
-// A small work-list image as a kernel parameter (merge.cu): one launch in
-// place of a staging copy. `bytes` is a multiple of 16, at most the capacity.
+// launch_merge behind the page-scaled prefill kernel.
+cudaError_t launch_merge_page8(const MergeParams& p, int n_rows, bool overlap, cudaStream_t stream);
+
+template <class... Args>
+cudaError_t launch_overlapping(void (*kern)(Args...), dim3 grid, int threads, size_t smem,
+                               bool overlap, cudaStream_t stream,
+                               const std::common_type_t<Args>&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// The work-list image of a page-scaled plan goes up by a kernel (merge.cu):
+// a small one as its parameter, a larger one read from pinned host memory.
+// `bytes` is a multiple of 16.
 constexpr size_t kImageParamBytes = 3840;
 struct ImageParam {
   uint32_t words[kImageParamBytes / 4];
 };
 cudaError_t launch_image(const ImageParam& image, size_t bytes, void* dst, cudaStream_t stream);
+cudaError_t launch_image_copy(const void* src, size_t bytes, void* dst, cudaStream_t stream);
 
 // fi_page_table_step (page_step.cu): the arguments of the call, and the step
 // workspace's error word and ticket.

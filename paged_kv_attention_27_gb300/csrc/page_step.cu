@@ -17,13 +17,14 @@
 // by the last block of a ticket counter (which wraps to zero) otherwise.
 //
 // Measured, calls back to back: 256 requests of up to 8K tokens and one new
-// token each (180 KB) 8.2 us, 1536 of 2048 requests with up to 64 new tokens
-// (1.3 MB) 12.3 us. Blocks of 512 threads with 2048 entries each; 1024 threads
+// token each (180 KB) 7.8 us, 1536 of 2048 requests with up to 64 new tokens
+// (1.3 MB) 12.2 us. Blocks of 512 threads with 2048 entries each; 1024 threads
 // and 4096 entries took 10.2 and 14.3 us (a barrier waits for twice the warps),
 // 256 threads 8.2 and 14.4 us.
 #include <cuda_runtime.h>
 
 #include "page8.cuh"
+#include "ptx_page8.cuh"
 
 namespace fi {
 
@@ -99,10 +100,12 @@ __global__ void __launch_bounds__(kThreads) page_step_kernel(PageStepParams p) {
   // consecutive requests per thread; the first one's loads go out at once
   const int per = (p.batch + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
-  const int head = p.ring_state[0], count = p.ring_state[1], cap = p.ring_capacity;
-
+  // (the launch may start beside the one in front of it)
+  dev::pdl_trigger();
   for (int i = tid; i < (p.max_requests + 31) / 32; i += kThreads) met[i] = 0u;
   if (tid == 0) err_sh = 0u;
+  dev::pdl_wait();
+  const int head = p.ring_state[0], count = p.ring_state[1], cap = p.ring_capacity;
   __syncthreads();
 
   uint32_t err = 0u;
@@ -309,13 +312,15 @@ cudaError_t launch(const PageStepParams& p, int grid, size_t smem, cudaStream_t 
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = unsigned(grid);
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = CLUSTER ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(grid);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CLUSTER ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 

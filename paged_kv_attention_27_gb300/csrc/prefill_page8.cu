@@ -8,7 +8,7 @@
 // only, the second stream of scores and outputs can take every other K/V tile
 // of the same rows (a tile's chain score -> softmax -> output is serial, and two
 // of them keep the SM busy); the two states are merged at the end. That is a
-// kernel of its own (SOLO): 48 drafts of 1-9 rows 158 -> 136 us, but launches
+// kernel of its own (SOLO): 48 drafts of 1-9 rows 158 -> 133 us, but launches
 // whose items fill both tiles 3 % slower, so the planner picks it where an
 // eighth of the work or more is in items of one M tile.
 //
@@ -37,6 +37,15 @@
 // overlap, and one warp per scheduler waits for its own instructions.) A warp
 // each to issue a tile's MMAs and one to copy K/V pages and their scales; a
 // warpgroup to turn q into terms and widen V.
+//
+// Measured, calls back to back: two chunks of 400-512 rows on 20000-32000 keys,
+// 64/8 heads of 128, 938 us (1000 TFLOP/s, 0.54 of the measured bf16 burst
+// rate); four prompts of 3300-4096 tokens 1008 us (0.52); 48 drafts of 1-9 rows
+// on 300-8192 keys, 32/8 heads, 133 us (0.28 of the copy bandwidth). Bound by
+// the chain of a tile: scores seen by the softmax, 1400 cycles of softmax, 300
+// until its P is seen, 1150 for the output MMAs until the next scores' may go,
+// 765 for those; the two M tiles' chains overlap, a pair takes 3850-4000 cycles,
+// 41 % of them with the tensor pipe busy.
 #include <cfloat>
 #include <climits>
 #include <type_traits>
@@ -169,7 +178,9 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
     atomicOr(prm.err, kErrTimeout);
   };
 
+  // (see the decode kernel)
   if (threadIdx.x == 0) {
+    pdl_trigger();
     for (int s = 0; s < kItemRing; ++s) {
       mbar_init(smem_u32(&bars.item_full[s]), 1);
       // softmax warps, MMA warps, the widening warps
@@ -200,6 +211,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
     tmem_alloc(smem_u32(&tmem_base_sh), C::TMEM_COLS);
     tmem_relinquish();
   }
+  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -922,7 +934,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
 
 template <int D, class E, bool SOLO>
 cudaError_t launch_t(const void* q, const CUtensorMap& km, const CUtensorMap& vm,
-                     const PrefillParams& p, int grid, cudaStream_t stream) {
+                     const PrefillParams& p, int grid, bool overlap, cudaStream_t stream) {
   using C = P8Cfg<D, E>;
   auto kern = prefill_page8_kernel<D, E, SOLO>;
   static std::atomic<uint64_t> configured{0};
@@ -935,19 +947,19 @@ cudaError_t launch_t(const void* q, const CUtensorMap& km, const CUtensorMap& vm
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (e != cudaSuccess) return e;
-  kern<<<grid, C::THREADS, C::SMEM, stream>>>(q, km, vm, p);
-  return cudaGetLastError();
+  return launch_overlapping(kern, grid, C::THREADS, C::SMEM, overlap, stream, q, km, vm, p);
 }
 
 template <class E>
 cudaError_t launch_d(int head_dim, bool solo, const void* q, const CUtensorMap& km,
-                     const CUtensorMap& vm, const PrefillParams& p, int grid, cudaStream_t stream) {
+                     const CUtensorMap& vm, const PrefillParams& p, int grid, bool overlap,
+                     cudaStream_t stream) {
   switch (head_dim) {
-    case 64: return solo ? launch_t<64, E, true>(q, km, vm, p, grid, stream)
-                         : launch_t<64, E, false>(q, km, vm, p, grid, stream);
-    case 128: return solo ? launch_t<128, E, true>(q, km, vm, p, grid, stream)
-                          : launch_t<128, E, false>(q, km, vm, p, grid, stream);
-    case 256: return launch_t<256, E, false>(q, km, vm, p, grid, stream);
+    case 64: return solo ? launch_t<64, E, true>(q, km, vm, p, grid, overlap, stream)
+                         : launch_t<64, E, false>(q, km, vm, p, grid, overlap, stream);
+    case 128: return solo ? launch_t<128, E, true>(q, km, vm, p, grid, overlap, stream)
+                          : launch_t<128, E, false>(q, km, vm, p, grid, overlap, stream);
+    case 256: return launch_t<256, E, false>(q, km, vm, p, grid, overlap, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -956,12 +968,13 @@ cudaError_t launch_d(int head_dim, bool solo, const void* q, const CUtensorMap& 
 
 cudaError_t launch_prefill_page8(int head_dim, int dtype, bool solo, const void* q,
                                  const CUtensorMap& km, const CUtensorMap& vm,
-                                 const PrefillParams& p, int num_sms, cudaStream_t stream) {
+                                 const PrefillParams& p, int num_sms, bool overlap,
+                                 cudaStream_t stream) {
   const int grid = p.n_items < num_sms ? p.n_items : num_sms;
   if (grid <= 0) return cudaSuccess;
   switch (dtype) {
-    case FI_DTYPE_BF16: return launch_d<Bf16>(head_dim, solo, q, km, vm, p, grid, stream);
-    case FI_DTYPE_FP16: return launch_d<Fp16>(head_dim, solo, q, km, vm, p, grid, stream);
+    case FI_DTYPE_BF16: return launch_d<Bf16>(head_dim, solo, q, km, vm, p, grid, overlap, stream);
+    case FI_DTYPE_FP16: return launch_d<Fp16>(head_dim, solo, q, km, vm, p, grid, overlap, stream);
     default: return cudaErrorInvalidValue;
   }
 }

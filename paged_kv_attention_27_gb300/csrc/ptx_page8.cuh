@@ -72,6 +72,15 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn, int b_
          (uint32_t(M >> 4) << 24);
 }
 
+// Programmatic dependent launch: the kernel behind this one may start (if its
+// launch says so) once every block has called pdl_trigger; what it reads of
+// earlier kernels' results it reads after pdl_wait, which returns when those
+// have completed (at once in an ordinary launch).
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Four bytes from global to shared memory, completing asynchronously; the
 // calling thread's copies so far arrive on an mbarrier when they have landed.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {

@@ -509,3 +509,52 @@ def test_cache_offsets_beyond_32_bits():
         out, lse = x.run(page_stride=stride)
         assert x.status() == B.FI_OK
         _page8.compare(b, out, lse, _page8.reference(b), what="far pages")
+
+
+def test_calls_back_to_back_in_one_workspace():
+    """Launches may start beside the ones in front of them: appends, small and
+    large plans of both modes, copies into q and out of the results, all in one
+    stream and workspace with nothing between them, against the same calls one
+    at a time."""
+    import torch
+    P, H, d = 16, 2, 128
+    shapes = [([300, 40], None), ([2000] * 60, None), ([700, 30], [90, 3]), ([900] * 12, [5] * 12),
+              ([5], None), ([4000], [600])]
+    batches = [_page8.Batch(kv, 8, H, d, P, qo_lens=qo, seed=20 + i) for i, (kv, qo) in enumerate(shapes)]
+    ws_bytes = max(_page8.Device(b).plan.workspace_bytes for b in batches)
+    step_ws = torch.zeros(B.FI_STEP_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rounds = 6
+    new = torch.randn(rounds, 8, 2 * H, d, device="cuda", generator=g).to(torch.bfloat16)
+    smap = [torch.arange(8, device="cuda") + int(b.page_indices[0]) * P for b in batches]
+
+    def go(wait):
+        ws = torch.zeros(ws_bytes, dtype=torch.uint8, device="cuda")
+        devs = [_page8.Device(b) for b in batches]
+        for x in devs:
+            x.workspace = ws
+        torch.cuda.synchronize()
+        outs = []
+        for r in range(rounds):
+            for x, m in zip(devs, smap):
+                # the first 8 keys of request 0 anew, then attention, then q from its result
+                B.fi_append_paged_kv(min(8, x.b.kv_lens[0]), m, new[r, :, :H], new[r, :, H:], 2 * H * d,
+                                     B.FI_DTYPE_BF16, H, d, x.k, x.v, B.FI_DTYPE_E4M3_PAGE,
+                                     B.FI_LAYOUT_NHD, 0, x.b.num_pages, P, x.ks, x.vs, step_ws)
+                if wait:
+                    torch.cuda.synchronize()
+                x.run()
+                if wait:
+                    torch.cuda.synchronize()
+                outs.append((x.out.clone(), x.lse.clone()))
+                x.q.add_(x.out)
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert B.fi_check_device_status(ws) == B.FI_OK
+        return outs
+
+    want = go(True)
+    for _ in range(3):
+        for (o, l), (wo, wl) in zip(go(False), want):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
