@@ -183,10 +183,12 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
     // two of its (larger) tiles: half as many items, and where a resident CTA's
     // share is a dozen tiles or less, one item each. (70B-shaped batch 164 us at
     // eight items per SM, 158 at four, 169 at two; one request of 30K keys 53 us
-    // in chunks of 512, 41 in one wave.)
+    // in chunks of 512, 41 in one wave.) With one CTA per SM, three items each:
+    // 56 windows of 4096 keys at head_dim 256 100.3 us, 103.3 with four.
     const int64_t slots = int64_t(num_sms) * page8_decode_ctas(head_dim);
+    const int64_t page8_items = int64_t(num_sms) * (page8_decode_ctas(head_dim) == 2 ? 4 : 3);
     const int64_t target = !page8 ? int64_t(num_sms) * 2 * 4
-                                  : dec_tiles <= 12 * slots ? slots : int64_t(num_sms) * 4;
+                                  : dec_tiles <= 12 * slots ? slots : page8_items;
     const int64_t min_chunk_tiles = std::max<int64_t>(1, 512 / tile);
     const int64_t chunk_tiles = std::max(min_chunk_tiles, ceil_div(dec_tiles, target));
     const int64_t chunk = chunk_tiles * tile;  // a multiple of the page size
