@@ -39,7 +39,7 @@
 // Measured, calls back to back with their work-list copies: 64 requests of
 // 512-4096 keys, 32/32 heads of 128 (828 MB) 132 us, 0.92 of the copy bandwidth;
 // 128 requests of 128-16384 keys, 64/8 heads (870 MB) 152 us, 0.84; 56 requests,
-// 16/8 heads of 256, fp16, window of 4096 (598 MB) 104.6 us, 0.84. Long keys
+// 16/8 heads of 256, fp16, window of 4096 (598 MB) 100.3 us, 0.88. Long keys
 // alone run at 0.97-0.99; the rest is items' starts and ends and the last items.
 #include <cfloat>
 #include <type_traits>

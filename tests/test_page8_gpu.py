@@ -558,3 +558,28 @@ def test_calls_back_to_back_in_one_workspace():
     for _ in range(3):
         for (o, l), (wo, wl) in zip(go(False), want):
             assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+def test_a_call_waits_for_both_streams_of_a_mixed_one():
+    """A mixed batch runs its decode rows on a side stream; the next call, in the
+    same workspace, comes after both. (The second plan is the smaller one in
+    every way.)"""
+    import torch
+    kv, qo = [400, 90] + [6000] * 24, [120, 90] + [1] * 24
+    x = _page8.Device(_page8.Batch(kv, 8, 2, 128, 16, qo_lens=qo, seed=30))
+    y = _page8.Device(_page8.Batch([70, 5], 8, 2, 128, 16, seed=31))
+    assert y.plan.workspace_bytes <= x.plan.workspace_bytes
+    y.workspace = x.workspace
+    want = []
+    for d in (x, y):
+        want.append([t.clone() for t in d.run()])
+        assert d.status() == B.FI_OK
+    for _ in range(30):
+        x.out.fill_(7)
+        y.out.fill_(7)
+        x.run()
+        y.run()
+        torch.cuda.synchronize()
+        for d, (o, l) in zip((x, y), want):
+            assert torch.equal(d.out, o) and torch.equal(d.lse, l)
+    assert x.status() == B.FI_OK
