@@ -8,7 +8,7 @@
 // only, the second stream of scores and outputs can take every other K/V tile
 // of the same rows (a tile's chain score -> softmax -> output is serial, and two
 // of them keep the SM busy); the two states are merged at the end. That is a
-// kernel of its own (SOLO): 48 drafts of 1-9 rows 158 -> 133 us, but launches
+// kernel of its own (SOLO): 48 drafts of 1-9 rows 158 -> 129 us, but launches
 // whose items fill both tiles 3 % slower, so the planner picks it where an
 // eighth of the work or more is in items of one M tile.
 //
@@ -35,13 +35,15 @@
 // while they are on one tile, the other's MMAs run. (A warpgroup per tile, a
 // thread per row, was slower: the warpgroups have to take turns for that
 // overlap, and one warp per scheduler waits for its own instructions.) A warp
-// each to issue a tile's MMAs and one to copy K/V pages and their scales; a
-// warpgroup to turn q into terms and widen V.
+// each to issue a tile's MMAs and one to copy K/V pages and their scales (two in
+// the SOLO kernel: a TMA box takes about 130 cycles to issue, so that one warp
+// was slower than its tiles, 133 -> 129 us; elsewhere a second one costs 0.4 %);
+// a warpgroup to turn q into terms and widen V.
 //
 // Measured, calls back to back: two chunks of 400-512 rows on 20000-32000 keys,
 // 64/8 heads of 128, 938 us (1000 TFLOP/s, 0.54 of the measured bf16 burst
 // rate); four prompts of 3300-4096 tokens 1008 us (0.52); 48 drafts of 1-9 rows
-// on 300-8192 keys, 32/8 heads, 133 us (0.28 of the copy bandwidth). Bound by
+// on 300-8192 keys, 32/8 heads, 129 us (0.29 of the copy bandwidth). Bound by
 // the chain of a tile: scores seen by the softmax, 1400 cycles of softmax, 300
 // until its P is seen, 1150 for the output MMAs until the next scores' may go,
 // 765 for those; the two M tiles' chains overlap, a pair takes 3850-4000 cycles,
@@ -129,6 +131,7 @@ __global__ void __launch_bounds__(P8Cfg<D, E>::THREADS, 1)
 prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map, PrefillParams prm) {
   using C = P8Cfg<D, E>;
+  constexpr int COPIERS = SOLO ? 2 : 1;   // warps that copy K/V pages
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) P8Barriers bars;
   __shared__ uint32_t tmem_base_sh;
@@ -183,17 +186,17 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
     pdl_trigger();
     for (int s = 0; s < kItemRing; ++s) {
       mbar_init(smem_u32(&bars.item_full[s]), 1);
-      // softmax warps, MMA warps, the widening warps
-      mbar_init(smem_u32(&bars.item_empty[s]), C::SOFT + C::TILES + 4);
+      // softmax warps, MMA warps, the widening warps, a second copying warp
+      mbar_init(smem_u32(&bars.item_empty[s]), C::SOFT + C::TILES + 4 + COPIERS - 1);
     }
     mbar_init(smem_u32(&bars.q_full), 4);
     mbar_init(smem_u32(&bars.q_empty), C::TILES);
     for (int s = 0; s < C::NK; ++s) {
-      mbar_init(smem_u32(&bars.k_full[s]), 1 + ppt);        // the bytes, and each page's scales
+      mbar_init(smem_u32(&bars.k_full[s]), COPIERS + ppt);  // the bytes, and each page's scales
       mbar_init(smem_u32(&bars.k_empty[s]), C::TILES + 4);  // S of the tiles; the scales' readers
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&bars.vr_full[s]), 1);
+      mbar_init(smem_u32(&bars.vr_full[s]), COPIERS);
       mbar_init(smem_u32(&bars.vr_empty[s]), 4);
       mbar_init(smem_u32(&bars.v_full[s]), 4);
       mbar_init(smem_u32(&bars.v_empty[s]), C::TILES);
@@ -437,8 +440,10 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
     if (!ok && lane == 0) fail();
   } else if (warp >= C::W_MMA) {
     setmaxnreg_dec<C::HELP_REGS>();
-    if (warp == C::W_KV) {
+    if (warp >= C::W_KV && warp < C::W_KV + COPIERS) {
       // -------------------------------------------------------------- K/V copies
+      // Each warp has its share of a tile's pages; the first hands out the items.
+      const int share = ppt / COPIERS, slot0 = (warp - C::W_KV) * share;
       if (lane == 0) {
         prefetch_tensormap(&k_map);
         prefetch_tensormap(&v_map);
@@ -454,6 +459,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
         return true;
       };
       auto next_item = [&](int n, int& idx) {
+        if (warp != C::W_KV) return take_item(n, idx);
         int v = -1;
         bool good = true;
         if (lane == 0) {
@@ -464,16 +470,16 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
         idx = __shfl_sync(0xffffffffu, v, 0);
         return __shfl_sync(0xffffffffu, good, 0) != 0;
       };
-      auto pages_in = [&](const WorkItem& w, int j) {
-        return (min(C::N, w.tok_end - w.tok_begin - j * C::N) + P - 1) / P;
+      // whether this lane has a page of tile j
+      auto has_page = [&](const WorkItem& w, int j) {
+        return lane < share && (slot0 + lane) * P < w.tok_end - w.tok_begin - j * C::N;
       };
       int it = -1, t = 0;
       bool ok = next_item(0, it);
       WorkItem w;
       if (ok && it >= 0) w = prm.items[it];
       int next_page = -1;
-      if (ok && it >= 0 && tiles_of(w) > 0 && lane < pages_in(w, 0))
-        next_page = prm.page_indices[w.page_begin + lane];
+      if (ok && it >= 0 && has_page(w, 0)) next_page = prm.page_indices[w.page_begin + slot0 + lane];
       for (int n = 0; ok && it >= 0; ++n) {
         const int nt = tiles_of(w);
         const int c1 = prm.layout == FI_LAYOUT_NHD ? w.head : 0;
@@ -485,21 +491,21 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
         }
         WorkItem wn;
         if (it_next >= 0) wn = prm.items[it_next];
-        const bool more = it_next >= 0 && tiles_of(wn) > 0;
         if (nt == 0)
-          next_page = more && lane < pages_in(wn, 0) ? prm.page_indices[wn.page_begin + lane] : -1;
+          next_page = it_next >= 0 && has_page(wn, 0) ? prm.page_indices[wn.page_begin + slot0 + lane]
+                                                      : -1;
         for (int j = 0; j < nt; ++j, ++t) {
           const int ks = t % C::NK, rs = t % C::NVR;
           const int page = next_page;
-          const bool mine = lane < pages_in(w, j);
+          const bool mine = has_page(w, j);
           const bool valid = mine && page >= 0 && page < prm.num_pages;
           if (mine && !valid) atomicOr(prm.err, kErrBounds);
           next_page = -1;
           if (j + 1 < nt) {
-            if (lane < pages_in(w, j + 1))
-              next_page = prm.page_indices[w.page_begin + (j + 1) * ppt + lane];
-          } else if (more && lane < pages_in(wn, 0)) {
-            next_page = prm.page_indices[wn.page_begin + lane];
+            if (has_page(w, j + 1))
+              next_page = prm.page_indices[w.page_begin + (j + 1) * ppt + slot0 + lane];
+          } else if (it_next >= 0 && has_page(wn, 0)) {
+            next_page = prm.page_indices[wn.page_begin + slot0 + lane];
           }
           const uint32_t bytes =
               uint32_t(__popc(__ballot_sync(0xffffffffu, valid))) * C::BLK * box;
@@ -513,20 +519,20 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
           if (lane == 0 && !skip) mbar_arrive_expect_tx(kf, bytes);
           __syncwarp();
           if (valid && !skip) {
-            const uint32_t dst = base + C::OFF_K + ks * C::CODES + lane * box;
+            const uint32_t dst = base + C::OFF_K + ks * C::CODES + (slot0 + lane) * box;
 #pragma unroll
             for (int b = 0; b < C::BLK; ++b)
               tma_load_4d(dst + b * C::N * 128, &k_map, kf, b * 128, c1, c2, page);
           }
-          if (lane < ppt) {
+          if (lane < share) {
             if (valid) {
               const size_t at = size_t(page) * hkv + w.head;
-              const uint32_t sc = smem_u32(&raw_scale[ks][lane]);
+              const uint32_t sc = smem_u32(&raw_scale[ks][slot0 + lane]);
               cp_async4(sc, prm.k_head_scale + at);
               cp_async4(sc + 4, prm.v_head_scale + at);
               cp_async_arrive(kf);
             } else {
-              raw_scale[ks][lane] = make_float2(-1.f, 1.f);
+              raw_scale[ks][slot0 + lane] = make_float2(-1.f, 1.f);
               mbar_arrive(kf);
             }
           }
@@ -540,7 +546,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
           if (lane == 0) mbar_arrive_expect_tx(vf, bytes);
           __syncwarp();
           if (valid) {
-            const uint32_t dst = base + C::OFF_VR + rs * C::CODES + lane * box;
+            const uint32_t dst = base + C::OFF_VR + rs * C::CODES + (slot0 + lane) * box;
 #pragma unroll
             for (int b = 0; b < C::BLK; ++b)
               tma_load_4d(dst + b * C::N * 128, &v_map, vf, b * 128, c1, c2, page);
@@ -919,7 +925,7 @@ prefill_page8_kernel(const void* q, const __grid_constant__ CUtensorMap k_map,
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
   // every copy that was issued lands before the CTA exits, also after a timeout
-  if (warp == C::W_KV && lane == 0) {
+  if (warp >= C::W_KV && warp < C::W_KV + COPIERS && lane == 0) {
     const bool no_v = issued < 0;   // of the last tile
     if (no_v) issued = -issued;
     for (int j = max(0, issued - C::NK); j < issued; ++j) {
