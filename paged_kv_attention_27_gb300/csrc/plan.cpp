@@ -173,6 +173,22 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
       dec_tiles += std::max<int64_t>(1, ceil_div(kv_len[b] - s0, tile)) * num_kv_heads;
     }
   }
+  // Single rows beside a page-scaled prefill: where they are little work, and
+  // none longer than the longest prefill request, they are items of the prefill
+  // kernel too. A launch of their own, forked and joined, costs about 4 us; a
+  // tile takes the prefill kernel about 0.8 us more of one SM than the decode
+  // kernel: four or five tiles per SM break even. (Two single rows among 48
+  // drafts, two tiles per SM: 128.6 us with two launches, 126.0 with one.)
+  bool single_rows_in_prefill = false;
+  if (page8 && mode == FI_MODE_PREFILL && !dec.empty() && dec_tiles <= 4 * int64_t(num_sms)) {
+    int64_t longest_dec = 0, longest = -1;
+    for (int b = 0; b < batch; ++b) {
+      int64_t& x = qo_len[b] == 1 ? longest_dec : longest;
+      if (qo_len[b] >= 1) x = std::max(x, kv_len[b] - first_key(b, 0));
+    }
+    single_rows_in_prefill = longest_dec <= longest;
+    if (single_rows_in_prefill) dec.clear();
+  }
   if (!dec.empty()) {
     // Aim for ~4 items per resident decode CTA (2 per SM), so that the
     // largest item is a small fraction of one CTA's share, but never cut
@@ -315,7 +331,7 @@ fi_status build_plan(int32_t mode, int32_t batch, const int32_t* qo_indptr,
   struct Tile { int64_t len, kv_begin, kv_end; int32_t b, qt; };
   std::vector<Tile> tiles;
   for (int b = 0; b < batch; ++b) {
-    if (qo_len[b] < 2) continue;
+    if (qo_len[b] < (single_rows_in_prefill ? 1 : 2)) continue;
     const int64_t n_qt = ceil_div(qo_len[b], tile_rows);
     for (int64_t qt = 0; qt < n_qt; ++qt) {
       const int64_t r0 = qt * tile_rows;

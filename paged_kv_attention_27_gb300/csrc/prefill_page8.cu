@@ -43,7 +43,7 @@
 // Measured, calls back to back: two chunks of 400-512 rows on 20000-32000 keys,
 // 64/8 heads of 128, 938 us (1000 TFLOP/s, 0.54 of the measured bf16 burst
 // rate); four prompts of 3300-4096 tokens 1008 us (0.52); 48 drafts of 1-9 rows
-// on 300-8192 keys, 32/8 heads, 129 us (0.29 of the copy bandwidth). Bound by
+// on 300-8192 keys, 32/8 heads, 126 us (0.30 of the copy bandwidth). Bound by
 // the chain of a tile: scores seen by the softmax, 1400 cycles of softmax, 300
 // until its P is seen, 1150 for the output MMAs until the next scores' may go,
 // 765 for those; the two M tiles' chains overlap, a pair takes 3850-4000 cycles,

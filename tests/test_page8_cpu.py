@@ -75,7 +75,7 @@ def test_work_lists_cover_every_row_and_key_once(seed):
         if t1 > t0:
             assert pb == b.page_indptr[req] + a // P and npg == -(-(t1 - a) // P)
         if not decode:
-            assert t0 % P == 0 and qo[req] > 1
+            assert t0 % P == 0 and qo[req] >= 1
             assert (row - b.qo_indptr[req]) % rows_per == 0
         m = 1 if decode else min(rows_per, int(b.qo_indptr[req + 1]) - row)
         for i in range(m):
@@ -95,3 +95,18 @@ def test_work_lists_cover_every_row_and_key_once(seed):
             first = max(0, pos - window) if window >= 0 else 0
             want += max(0, last + 1 - first) * hkv
     assert len(seen) == want and all(c == 1 for c in seen.values())
+
+
+def test_single_rows_beside_a_prefill():
+    """Few and short ones are prefill items; many, or one longer than any prefill
+    request, stay decode work, and so do those of a batch without longer rows."""
+    def decode_items(kv, qo):
+        b = _page8.Batch(kv, 8, 2, 64, 16, qo_lens=qo, seed=1)
+        info = B.fi_plan_get_info(b.plan(B, 20))
+        assert info["num_decode_items"] + info["num_prefill_items"] > 0
+        return info["num_decode_items"]
+    assert decode_items([500, 400, 500], [5, 1, 1]) == 0
+    assert decode_items([500, 501], [5, 1]) > 0
+    assert decode_items([2000] + [1900] * 3, [5] + [1] * 3) > 0     # 3 * 15 tiles * 2 heads > 4 * 20
+    assert decode_items([2000] + [1900] * 2, [5] + [1] * 2) == 0
+    assert decode_items([40, 30, 0], [1, 1, 0]) > 0
