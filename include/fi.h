@@ -226,7 +226,8 @@ fi_status fi_plan_get_info(fi_plan_t plan, fi_plan_info* info);
  * group index, keys within the group's prefix, slot = the state slot of
  * row 0 of q). The prefill items of an FI_DTYPE_E4M3_PAGE plan name a kv_head
  * with all its query heads, too: 256 / g rows of q per item (128 / g at
- * head_dim 256).
+ * head_dim 256); few and short single rows beside longer ones are prefill
+ * items there.
  * `capacity` is in items; *num_items receives the plan's item count.
  */
 fi_status fi_plan_get_work(fi_plan_t plan, int32_t* items_h, int32_t capacity,
